@@ -8,8 +8,11 @@
 #include <mutex>
 
 #include "../../include/delta_rule.h"
+#include "attn_decode.cuh"
 #include "decode.cuh"
+#include "pages.cuh"
 #include "prepost.cuh"
+#include "qkrope.cuh"
 #include "shortconv.cuh"
 #include "clvr.cuh"
 #include "dr_common.cuh"
@@ -830,6 +833,169 @@ extern "C" int delta_rule_clvr_bwd(const void *u, const void *W, const void *dh_
     if (rc != DR_OK) return rc;
     return clvr_bwd_run(u, W, dh_out, du, dW, M, K, N, dtype == DR_BF16, workspace, ws_bytes_given,
                         (cudaStream_t)stream);
+}
+
+// ---- the softmax-attention layers beside the delta rule: cache pages, query/key norm with the
+// rotation, decoding attention over the paged cache ----
+
+extern "C" int delta_rule_pages(const int *cached, const int *fresh, const int *free_pages, const int *n_free,
+                                int *table, int *lens, int *cu_new, int *positions, long long *slots, int *n_left,
+                                int R, int F, int width, int page, int N, void *stream) {
+    if (R < 0 || F < 0 || width < 0 || page <= 0 || N < 0) return DR_ERR_ARG;
+    if (R > PAGES_MAX_REQUESTS || N > (1 << 30)) return DR_ERR_UNSUPPORTED;
+    if (!n_free || !cu_new || !n_left) return DR_ERR_ARG;
+    if (R > 0 && (!cached || !fresh || !lens || (width > 0 && !table))) return DR_ERR_ARG;
+    if ((F > 0 && !free_pages) || (N > 0 && (!positions || !slots))) return DR_ERR_ARG;
+    const void *ints[] = {cached, fresh, free_pages, n_free, table, lens, cu_new, positions, n_left};
+    for (const void *p : ints)
+        if ((uintptr_t)p & 3u) return DR_ERR_ALIGN;
+    if ((uintptr_t)slots & 7u) return DR_ERR_ALIGN;
+    Pages p = {};
+    p.cached = cached; p.fresh = fresh; p.free_pages = free_pages; p.n_free = n_free; p.table = table;
+    p.lens = lens; p.cu_new = cu_new; p.positions = positions; p.n_left = n_left; p.slots = slots;
+    p.R = R; p.F = F; p.width = width; p.page = page; p.N = N;
+    return launch_status(pages_run(p, (cudaStream_t)stream));
+}
+
+// A stride in elements: 16-byte rows, no overlap.
+static int check_stride(long long stride, long long least, int dtype) {
+    if (stride < least || stride > (1LL << 48)) return DR_ERR_ARG;
+    return stride % (dtype == DR_BF16 ? 8 : 4) ? DR_ERR_ALIGN : DR_OK;
+}
+
+// Checks shared by the three forms of the norm with rotation; fills what they share.
+static int check_qkrope(int B, int T, int Hq, int Hk, int d, int rot, int interleaved, int dtype, const void *q,
+                        const void *k, const float *wq, const float *wk, const double *inv_freq,
+                        const int *positions, long long q_stride, long long k_stride, QkRope *p) {
+    size_t rows = 0;
+    const int rc = check_rows(B, T, 1, d, dtype, &rows);
+    if (rc != DR_OK) return rc;
+    if (Hq < 0 || Hk < 0 || rot < 0 || rot > d || (interleaved != 0 && interleaved != 1)) return DR_ERR_ARG;
+    if (Hq > 1024 || Hk > 1024 || Hq + Hk > 1024 || rot % 16 != 0) return DR_ERR_UNSUPPORTED;
+    if ((Hq > 0 && !q) || (Hk > 0 && !k) || (rot > 0 && !inv_freq)) return rows == 0 ? DR_OK : DR_ERR_ARG;
+    int sc = Hq > 0 ? check_stride(q_stride, (long long)Hq * d, dtype) : DR_OK;
+    if (sc == DR_OK && Hk > 0) sc = check_stride(k_stride, (long long)Hk * d, dtype);
+    if (sc != DR_OK) return sc;
+    const void *vec[] = {q, k, wq, wk};
+    for (const void *x : vec)
+        if (x && !aligned16(x)) return DR_ERR_ALIGN;
+    if ((uintptr_t)inv_freq & 7u || (uintptr_t)positions & 3u) return DR_ERR_ALIGN;
+    p->q = q; p->k = k; p->qs = q_stride; p->ks = k_stride; p->wq = wq; p->wk = wk; p->inv_freq = inv_freq;
+    p->pos = positions; p->N = rows; p->T = T; p->Hq = Hq; p->Hk = Hk; p->d = d; p->rot = rot;
+    p->interleaved = interleaved != 0;
+    return DR_OK;
+}
+
+extern "C" int delta_rule_qkrope(const void *q, const void *k, const float *wq, const float *wk,
+                                 const double *inv_freq, const int *positions, void *q_out, void *k_out, int B,
+                                 int T, int Hq, int Hk, int d, int rot, int interleaved, long long q_stride,
+                                 long long k_stride, int dtype, void *stream) {
+    QkRope p = {};
+    const int rc = check_qkrope(B, T, Hq, Hk, d, rot, interleaved, dtype, q, k, wq, wk, inv_freq, positions, q_stride,
+                                k_stride, &p);
+    if (rc != DR_OK || p.N == 0 || Hq + Hk == 0) return rc;
+    if ((Hq > 0 && !q_out) || (Hk > 0 && !k_out)) return DR_ERR_ARG;
+    if (!aligned16(q_out) || !aligned16(k_out)) return DR_ERR_ALIGN;
+    p.qo = q_out; p.ko = k_out;
+    return launch_status(qkrope_run(p, dtype == DR_BF16, (cudaStream_t)stream));
+}
+
+extern "C" int delta_rule_qkrope_cache(const void *q, const void *k, const void *v, const float *wq,
+                                       const float *wk, const double *inv_freq, const int *positions,
+                                       const long long *slots, void *q_out, void *k_cache, void *v_cache, int N,
+                                       int Hq, int Hk, int d, int rot, int interleaved, long long q_stride,
+                                       long long k_stride, long long v_stride, int n_pages, int page,
+                                       long long k_page_stride, long long v_page_stride, int dtype, void *stream) {
+    QkRope p = {};
+    int rc = check_qkrope(1, N, Hq, Hk, d, rot, interleaved, dtype, q, k, wq, wk, inv_freq, positions, q_stride,
+                          k_stride, &p);
+    if (rc != DR_OK) return rc;
+    if (Hk < 1 || n_pages < 0 || page <= 0) return DR_ERR_ARG;
+    if (N == 0) return DR_OK;
+    if (!positions || !slots || !v || !k_cache || !v_cache || (Hq > 0 && !q_out)) return DR_ERR_ARG;
+    const long long strides[] = {v_stride, k_page_stride, v_page_stride};
+    for (int i = 0; i < 3; ++i) {
+        rc = check_stride(strides[i], (long long)Hk * d * (i == 0 ? 1 : page), dtype);
+        if (rc != DR_OK) return rc;
+    }
+    if (!aligned16(v) || !aligned16(q_out) || !aligned16(k_cache) || !aligned16(v_cache) || (uintptr_t)slots & 7u)
+        return DR_ERR_ALIGN;
+    p.v = v; p.vs = v_stride; p.slots = slots; p.qo = q_out; p.kc = k_cache; p.vc = v_cache; p.kps = k_page_stride;
+    p.vps = v_page_stride; p.n_slots = (long long)n_pages * page; p.page = page;
+    return launch_status(qkrope_run(p, dtype == DR_BF16, (cudaStream_t)stream));
+}
+
+extern "C" size_t delta_rule_qkrope_workspace_size(int d) {
+    return d == 64 || d == 128 ? qkrope_ws_bytes(d) : (size_t)-1;
+}
+
+extern "C" int delta_rule_qkrope_bwd(const void *q, const void *k, const float *wq, const float *wk,
+                                     const double *inv_freq, const int *positions, const void *dq_out,
+                                     const void *dk_out, void *dq, void *dk_, float *dwq, float *dwk, int B, int T,
+                                     int Hq, int Hk, int d, int rot, int interleaved, long long q_stride,
+                                     long long k_stride, long long dq_stride, long long dk_stride, int dtype,
+                                     void *workspace, size_t ws_bytes_given, void *stream) {
+    QkRope p = {};
+    int rc = check_qkrope(B, T, Hq, Hk, d, rot, interleaved, dtype, q, k, wq, wk, inv_freq, positions, q_stride,
+                          k_stride, &p);
+    if (rc != DR_OK) return rc;
+    if (!aligned_elem(dwq, DR_F32) || !aligned_elem(dwk, DR_F32)) return DR_ERR_ALIGN;
+    if ((size_t)B * T == 0 || Hq + Hk == 0) {  // no rows: the weights' gradients are empty sums
+        cudaError_t e = cudaSuccess;
+        if (dwq) e = cudaMemsetAsync(dwq, 0, d * sizeof(float), (cudaStream_t)stream);
+        if (dwk && e == cudaSuccess) e = cudaMemsetAsync(dwk, 0, d * sizeof(float), (cudaStream_t)stream);
+        return launch_status(e);
+    }
+    if ((Hq > 0 && (!dq_out || !dq)) || (Hk > 0 && (!dk_out || !dk_))) return DR_ERR_ARG;
+    if (Hq > 0) rc = check_stride(dq_stride, (long long)Hq * d, dtype);
+    if (rc == DR_OK && Hk > 0) rc = check_stride(dk_stride, (long long)Hk * d, dtype);
+    if (rc != DR_OK) return rc;
+    if (!aligned16(dq_out) || !aligned16(dk_out) || !aligned16(dq) || !aligned16(dk_)) return DR_ERR_ALIGN;
+    if (dwq || dwk) {
+        rc = check_buffer(workspace, ws_bytes_given, qkrope_ws_bytes(d));
+        if (rc != DR_OK) return rc;
+    }
+    p.gq = dq_out; p.gk = dk_out; p.dq = dq; p.dk = dk_; p.dqs = dq_stride; p.dks = dk_stride; p.dwq = dwq;
+    p.dwk = dwk; p.part = (float *)workspace;
+    return launch_status(qkrope_bwd_run(p, dtype == DR_BF16, (cudaStream_t)stream));
+}
+
+static int check_attn(int Hq, int Hk, int d, int dtype) {
+    if (Hq <= 0 || Hk <= 0 || Hq % Hk != 0 || d <= 0) return DR_ERR_ARG;
+    if (dtype != DR_F32 && dtype != DR_BF16) return DR_ERR_ARG;
+    if ((d != 64 && d != 128) || Hq > 65535) return DR_ERR_UNSUPPORTED;
+    return DR_OK;
+}
+
+extern "C" size_t delta_rule_attn_decode_workspace_size(int Hq, int Hk, int d, int dtype) {
+    return check_attn(Hq, Hk, d, dtype) == DR_OK ? attn_decode_ws_bytes(Hq, Hk, d, dtype == DR_BF16) : (size_t)-1;
+}
+
+extern "C" int delta_rule_attn_decode(const void *q, const void *k_cache, const void *v_cache, const int *table,
+                                      const int *lens, void *out, float *lse, int R, int Hq, int Hk, int d,
+                                      int n_pages, int page, int width, long long k_page_stride,
+                                      long long v_page_stride, float scale, int window, int dtype, void *workspace,
+                                      size_t ws_bytes_given, void *stream) {
+    int rc = check_attn(Hq, Hk, d, dtype);
+    if (rc != DR_OK) return rc;
+    if (R < 0 || n_pages < 0 || page <= 0 || width < 0 || window < 0) return DR_ERR_ARG;
+    if (R == 0) return DR_OK;
+    if (!q || !lens || !out || (width > 0 && !table) || (n_pages > 0 && (!k_cache || !v_cache))) return DR_ERR_ARG;
+    rc = check_stride(k_page_stride, (long long)page * Hk * d, dtype);
+    if (rc == DR_OK) rc = check_stride(v_page_stride, (long long)page * Hk * d, dtype);
+    if (rc != DR_OK) return rc;
+    const void *vec[] = {q, k_cache, v_cache, out};
+    for (const void *x : vec)
+        if (!aligned16(x)) return DR_ERR_ALIGN;
+    if ((uintptr_t)table & 3u || (uintptr_t)lens & 3u || (uintptr_t)lse & 3u) return DR_ERR_ALIGN;
+    const bool bf16 = dtype == DR_BF16;
+    rc = check_buffer(workspace, ws_bytes_given, attn_decode_ws_bytes(Hq, Hk, d, bf16));
+    if (rc != DR_OK) return rc;
+    AttnDecode p = {};
+    p.q = q; p.kc = k_cache; p.vc = v_cache; p.table = table; p.lens = lens; p.out = out; p.lse = lse;
+    p.kps = k_page_stride; p.vps = v_page_stride; p.R = R; p.Hq = Hq; p.Hk = Hk; p.d = d; p.page = page;
+    p.n_pages = n_pages; p.width = width; p.window = window; p.scale = scale; p.ws = workspace;
+    return launch_status(attn_decode_run(p, bf16, (cudaStream_t)stream));
 }
 
 // Self-test of the bounded waits: one thread waits for an mbarrier phase that nothing

@@ -1,0 +1,697 @@
+// attn_decode.cu -- softmax attention of one new token per request over a paged key-value cache.
+//
+// For request r with n = lens[r] cached tokens (the new one among them) and query head h of the
+// group that shares key head h / (Hq / Hk), over the tokens t in [max(0, n - window), n):
+//   s_t = scale q . k_t,  o = sum_t e^{s_t} v_t / sum_t e^{s_t},  lse = log sum_t e^{s_t}
+// formed in one pass over the cache with the running maximum m and sum l of each head (in base 2:
+// s_t log2 e), fp32 throughout.
+//
+// What bounds it is reading the cache once: a key head's rows serve the G = Hq / Hk heads of its
+// group, 2 G flops a byte in bf16, far below what the tensor cores need to be busy; so the design
+// is about bytes in flight and an even split.
+//   Work.  The unit is a tile of 16 tokens of one (request, key head[, block of its query heads]).
+//     The tiles of all requests form one list, cut into equal contiguous runs, one per CTA, however
+//     ragged the lengths: a run may hold parts of several (request, head) segments.  A segment
+//     inside one CTA's run is finished there; one that crosses runs leaves fp32 partials (m, l, o)
+//     in the workspace, at most two a CTA, which k_attn_join adds in the order of the runs (no
+//     atomics: results do not change from run to run).
+//   Loads.  Each warp takes every fourth tile of its CTA's run through a pipeline of its own in
+//     shared memory, 16-byte asynchronous copies, rows swizzled by 16-byte chunk; the pipeline
+//     runs on across segments, and warps meet only at a segment's end.
+//   bf16.  The tile's tokens are the rows (M = 16) of mma.m16n8k16, the group's query heads its
+//     columns: S^T = K Q^T, then o^T = V^T P^T with P^T transposed in registers.  A group of up to
+//     8 heads is one n8 column block, of 16 two (larger groups are taken 16 heads at a time, and
+//     their rows read again for each block), so no row is spent on padding to 16 heads, and tcgen05's
+//     smallest tile (64 or 128 rows through tensor memory) would be mostly padding.  P is split
+//     into two bf16 numbers (high and rest, 2^-17 of p) and multiplied twice: rounding P once
+//     would put as large an error in the output as its own rounding, and the second product is
+//     hidden behind the loads.
+//   fp32.  CUDA cores, up to 8 heads at a time: a lane holds half a token's channels for the
+//     scores, 1/32 of the channels of every head for the output.
+// Tokens that are masked (or whose table entry is no page) are neither read nor seen: their rows
+// in shared memory are zero-filled, their scores -inf.  A request with none gives o = 0, lse = -inf.
+#include <math_constants.h>
+
+#include "attn_decode.cuh"
+
+namespace dr {
+namespace ad {
+
+constexpr int WARPS = 4, THREADS = WARPS * 32;
+constexpr int TILE = 16;          // tokens a warp takes at a time
+constexpr int MAX_CTAS = 296;     // two a SM (one where registers or shared memory hold no second)
+constexpr int MIN_TILES = WARPS;  // a CTA's run is at least one tile a warp
+constexpr float LOG2E = 1.44269504088896340736f, LN2 = 0.69314718055994530942f;
+
+struct Args {
+    AttnDecode a;
+    int G, GB, RB;       // query heads of a group; heads of a block; blocks of a group
+    float *part;         // [2 * MAX_CTAS][GB][D + 2]: o (not divided by l), m, l
+    int4 *head;          // [MAX_CTAS]: the split segment that begins in a CTA: request, key head, block, last CTA
+    float scale2;
+};
+
+__device__ __forceinline__ uint32_t smem_u32(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
+// 16 bytes, or 16 zero bytes (nothing is read then)
+__device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool live) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+__device__ __forceinline__ void ldsm4(uint32_t *r, uint32_t a) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t *r, uint32_t a) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+}
+__device__ __forceinline__ void mma(float *c, const uint32_t *a, uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t trans8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t pack(float lo, float hi) {
+    const __nv_bfloat162 x = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&x);
+}
+
+// a partial sum l at maximum m, at the joint maximum mx (l = 0: nothing seen, m = -inf; a NaN stays)
+__device__ __forceinline__ float part_of(float l, float m, float mx) { return l == 0.f ? 0.f : l * ex2(m - mx); }
+
+// The visible tokens of request r and its tiles.
+struct Span {
+    int first, n, tile0, tiles;
+    __device__ __forceinline__ void set(const AttnDecode &a, int r) {
+        const long long room = (long long)a.width * a.page;
+        n = max(a.lens[r], 0);
+        if (n > room) n = (int)room;
+        first = a.window > 0 && n > a.window ? n - a.window : 0;
+        tile0 = first / TILE;
+        tiles = n > first ? (n - 1) / TILE - tile0 + 1 : 0;
+    }
+};
+
+// A place in the list of tiles: request r, segment (key head, block of query heads) of it, tile.
+struct Place {
+    int r, seg, tile;
+    Span sp;
+};
+
+// What the CTA does: its run [a0, a1) of the list, the place of a0, and where a0's segment began.
+struct Run {
+    long long a0, a1, per;
+    int r0;
+    long long base;  // the list's index of request r0's first tile
+};
+
+// All threads of the CTA; every CTA finds its run from the lengths alone.
+__device__ __forceinline__ Run find_run(const Args &x, int segs) {
+    __shared__ long long wsum[WARPS], found[2];
+    const AttnDecode &a = x.a;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int each = (a.R + THREADS - 1) / THREADS, b0 = min(a.R, tid * each), b1 = min(a.R, b0 + each);
+    long long mine = 0;
+    Span sp;
+    for (int r = b0; r < b1; ++r) {
+        sp.set(a, r);
+        mine += (long long)sp.tiles * segs;
+    }
+    long long inc = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += y;
+    }
+    if (lane == 31) wsum[warp] = inc;
+    __syncthreads();
+    long long before = inc - mine, total = 0;
+    for (int w = 0; w < WARPS; ++w) {
+        if (w < warp) before += wsum[w];
+        total += wsum[w];
+    }
+    Run run;
+    run.per = max((long long)MIN_TILES, (total + gridDim.x - 1) / gridDim.x);
+    run.a0 = min(total, run.per * blockIdx.x);
+    run.a1 = min(total, run.a0 + run.per);
+    if (run.a0 < run.a1 && before <= run.a0 && run.a0 < before + mine) {
+        int r = b0;
+        for (; r < b1; ++r) {
+            sp.set(a, r);
+            const long long w = (long long)sp.tiles * segs;
+            if (run.a0 < before + w) break;
+            before += w;
+        }
+        found[0] = r;
+        found[1] = before;
+    }
+    __syncthreads();
+    run.r0 = run.a0 < run.a1 ? (int)found[0] : 0;
+    run.base = run.a0 < run.a1 ? found[1] : 0;
+    return run;
+}
+
+__device__ __forceinline__ void skip_empty(Place &pl, const AttnDecode &a) {
+    while (pl.sp.tiles == 0 && pl.r + 1 < a.R) pl.sp.set(a, ++pl.r);
+}
+// moves `by` tiles on; only called while the place stays inside the list
+__device__ __forceinline__ void advance(Place &pl, int by, int segs, const AttnDecode &a) {
+    pl.tile += by;
+    while (pl.tile >= pl.sp.tiles) {
+        pl.tile -= pl.sp.tiles;
+        if (++pl.seg == segs) {
+            pl.seg = 0;
+            if (pl.r + 1 >= a.R) return;
+            pl.sp.set(a, ++pl.r);
+            skip_empty(pl, a);
+            if (pl.sp.tiles == 0) return;
+        }
+    }
+}
+
+// One warp's pipeline of tiles.  A stage is the K rows, then the V rows, of 16 tokens.
+template <typename E, int D, int STAGES> struct Pipe {
+    static constexpr int ROW = D * (int)sizeof(E), CPR = ROW / 16;  // bytes, 16-byte chunks of a row
+    static constexpr int HALF = TILE * ROW, STAGE = 2 * HALF;
+    static constexpr int RPI = 32 / (CPR < 32 ? CPR : 32);          // rows a warp copies with one instruction
+    static_assert(CPR <= 32, "a row is at most one instruction");
+
+    // 16-byte chunk c of row r: the chunk index is exclusive-ored with the row's low bits, so that
+    // eight rows at one chunk lie in eight different banks groups
+    static __device__ __forceinline__ uint32_t at(int r, int c) { return r * ROW + ((c ^ (r & 7)) << 4); }
+
+    // copies the tile at pl into the stage; returns the bits of its live tokens
+    static __device__ __forceinline__ uint32_t load(uint32_t stage, const Args &x, const Place &pl) {
+        const AttnDecode &a = x.a;
+        const int lane = threadIdx.x & 31, h = pl.seg / x.RB;
+        const int t = (pl.sp.tile0 + pl.tile) * TILE + (lane & 15);
+        int pg = -1, in = 0;
+        if (t >= pl.sp.first && t < pl.sp.n) {
+            const int col = t / a.page;
+            in = t - col * a.page;
+            pg = a.table[(size_t)pl.r * a.width + col];
+            if (pg >= a.n_pages) pg = -1;
+        }
+        const uint32_t live = __ballot_sync(0xffffffffu, pg >= 0) & 0xffffu;
+        const int c = lane % CPR, row0 = lane / CPR;
+        const size_t inside = ((size_t)in * a.Hk + h) * D;
+        const size_t ko = pg < 0 ? 0 : (size_t)pg * a.kps + inside, vo = pg < 0 ? 0 : (size_t)pg * a.vps + inside;
+#pragma unroll
+        for (int i = 0; i < TILE; i += RPI) {
+            const int row = i + row0;
+            const size_t k = __shfl_sync(0xffffffffu, ko, row), v = __shfl_sync(0xffffffffu, vo, row);
+            const bool ok = live >> row & 1;
+            cp16(stage + at(row, c), (const E *)a.kc + k + c * (16 / (int)sizeof(E)), ok);
+            cp16(stage + HALF + at(row, c), (const E *)a.vc + v + c * (16 / (int)sizeof(E)), ok);
+        }
+        return live;
+    }
+};
+
+// ------------------------------------------------------------------ one warp's arithmetic
+// Each keeps, for the heads of a block, m (base 2), l and o, and offers
+//   start(q row of the block's first head, heads), tile(stage, live), finish(): l summed over lanes,
+//   each(f): f(head, channel, o) for every value the lane holds, and m / l of a head by stat().
+
+template <int D, int NT> struct Mma {  // bf16: blocks of 8 NT heads
+    typedef __nv_bfloat16 E;
+    static constexpr int GB = 8 * NT, STAGES = (D == 128 ? 3 : 6), CTAS = MAX_CTAS;
+    typedef Pipe<E, D, STAGES> P;
+    uint32_t q[D / 16][NT][2];
+    float o[D / 16][NT][4], m[NT][2], l[NT][2];
+
+    __device__ __forceinline__ void start(const E *src, int heads) {
+        const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                const bool in = j * 8 + g < heads;
+                const E *s = src + (in ? j * 8 + g : 0) * D + k * 16 + 2 * t;
+                q[k][j][0] = in ? *reinterpret_cast<const uint32_t *>(s) : 0u;
+                q[k][j][1] = in ? *reinterpret_cast<const uint32_t *>(s + 8) : 0u;
+            }
+        clear();
+    }
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+            m[j][0] = m[j][1] = -CUDART_INF_F;
+            l[j][0] = l[j][1] = 0.f;
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) o[k][j][0] = o[k][j][1] = o[k][j][2] = o[k][j][3] = 0.f;
+        }
+    }
+    __device__ __forceinline__ void tile(uint32_t stage, uint32_t live, float scale2, void *) {
+        const int lane = threadIdx.x & 31, g = lane >> 2;
+        // scores of token g (0, 1) and g + 8 (2, 3), heads 2 t and 2 t + 1 of each block of 8; two
+        // accumulators, so that half as many products wait on one another
+        float s[NT][4], s1[NT][4];
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[j][i] = s1[j][i] = 0.f;
+#pragma unroll
+        for (int k = 0; k < D / 16; k += 2) {
+            uint32_t a[4], b[4];
+            ldsm4(a, stage + P::at(lane & 15, k * 2 + (lane >> 4)));
+            ldsm4(b, stage + P::at(lane & 15, k * 2 + 2 + (lane >> 4)));
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                mma(s[j], a, q[k][j][0], q[k][j][1]);
+                mma(s1[j], b, q[k + 1][j][0], q[k + 1][j][1]);
+            }
+        }
+        const bool lo = live >> g & 1, hi = live >> (g + 8) & 1;
+        float mx[NT][2];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                s[j][i] = lo ? (s[j][i] + s1[j][i]) * scale2 : -CUDART_INF_F;
+                s[j][i + 2] = hi ? (s[j][i + 2] + s1[j][i + 2]) * scale2 : -CUDART_INF_F;
+                mx[j][i] = fmaxf(s[j][i], s[j][i + 2]);
+            }
+        }
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1)
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                mx[j][0] = fmaxf(mx[j][0], __shfl_xor_sync(0xffffffffu, mx[j][0], d));
+                mx[j][1] = fmaxf(mx[j][1], __shfl_xor_sync(0xffffffffu, mx[j][1], d));
+            }
+        bool up = false;
+#pragma unroll
+        for (int j = 0; j < NT; ++j) up = up || mx[j][0] > m[j][0] || mx[j][1] > m[j][1];
+        if (__any_sync(0xffffffffu, up)) {
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const float mn = fmaxf(m[j][i], mx[j][i]);
+                    const float f = m[j][i] == mn ? 1.f : ex2(m[j][i] - mn);  // equal: both may be -inf
+                    m[j][i] = mn;
+                    l[j][i] *= f;
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k) {
+                        o[k][j][i] *= f;
+                        o[k][j][i + 2] *= f;
+                    }
+                }
+        }
+        uint32_t ph[NT][2], pl[NT][2];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+            float p[4], rest[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                // -inf minus -inf (nothing seen yet) must not be NaN
+                p[i] = s[j][i] == -CUDART_INF_F ? 0.f : ex2(s[j][i] - m[j][i & 1]);
+                l[j][i & 1] += p[i];
+            }
+            ph[j][0] = pack(p[0], p[1]);
+            ph[j][1] = pack(p[2], p[3]);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                rest[2 * i] = p[2 * i] - __uint_as_float(ph[j][i] << 16);
+                rest[2 * i + 1] = p[2 * i + 1] - __uint_as_float(ph[j][i] & 0xFFFF0000u);
+                pl[j][i] = trans8(pack(rest[2 * i], rest[2 * i + 1]));
+                ph[j][i] = trans8(ph[j][i]);
+            }
+        }
+        const uint32_t v = stage + P::HALF;
+        const int row = (lane & 7) + ((lane >> 4) << 3), c0 = lane >> 3 & 1;
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+            uint32_t a[4];
+            ldsm4t(a, v + P::at(row, 2 * k + c0));
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                mma(o[k][j], a, ph[j][0], ph[j][1]);
+                mma(o[k][j], a, pl[j][0], pl[j][1]);
+            }
+        }
+    }
+    __device__ __forceinline__ void finish() {
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1)
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                l[j][0] += __shfl_xor_sync(0xffffffffu, l[j][0], d);
+                l[j][1] += __shfl_xor_sync(0xffffffffu, l[j][1], d);
+            }
+    }
+    // the heads of which the lane holds values: 2 NT
+    static constexpr int HEADS = 2 * NT, VALS = HEADS * (D / 8);
+    static __device__ __forceinline__ int head_of(int i) { return (i >> 1) * 8 + 2 * (threadIdx.x & 3) + (i & 1); }
+    __device__ __forceinline__ float &mm(int i) { return m[i >> 1][i & 1]; }
+    __device__ __forceinline__ float &ll(int i) { return l[i >> 1][i & 1]; }
+    template <typename F> __device__ __forceinline__ void each(F f) {
+        const int g = (threadIdx.x & 31) >> 2;
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    f(2 * j + (i & 1), head_of(2 * j + (i & 1)), k * 16 + g + (i >> 1) * 8, o[k][j][i]);
+    }
+    static constexpr int EXTRA = 0;  // bytes of shared memory of the warp's own
+};
+
+template <int D> struct Simt {  // fp32: blocks of 8 heads
+    typedef float E;
+    static constexpr int GB = 8, STAGES = (D == 128 ? 3 : 6), CTAS = MAX_CTAS / 2, NC = D / 32;
+    typedef Pipe<E, D, STAGES> P;
+    float o[GB][NC], m[GB], l[GB];
+    static constexpr int EXTRA = (GB * D + TILE * GB) * 4;  // the block's queries, the tile's p
+
+    float *qs, *ps;
+    __device__ __forceinline__ void start(const E *src, int heads) {
+        const int lane = threadIdx.x & 31;
+        __syncwarp();
+        for (int i = lane; i < GB * D; i += 32) qs[i] = i / D < heads ? src[i] : 0.f;
+        __syncwarp();
+        clear();
+    }
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int h = 0; h < GB; ++h) {
+            m[h] = -CUDART_INF_F;
+            l[h] = 0.f;
+#pragma unroll
+            for (int c = 0; c < NC; ++c) o[h][c] = 0.f;
+        }
+    }
+    __device__ __forceinline__ void tile(uint32_t, uint32_t live, float scale2, const char *base) {
+        const int lane = threadIdx.x & 31, t = lane & 15, half = lane >> 4;
+        float s[GB] = {};
+#pragma unroll 4
+        for (int c = 0; c < D / 8; ++c) {
+            const int ch = half * (D / 8) + c;
+            const float4 k = *reinterpret_cast<const float4 *>(base + P::at(t, ch));
+#pragma unroll
+            for (int h = 0; h < GB; ++h) {
+                const float4 q = *reinterpret_cast<const float4 *>(qs + h * D + 4 * ch);
+                s[h] += k.x * q.x + k.y * q.y + k.z * q.z + k.w * q.w;
+            }
+        }
+        const bool ok = live >> t & 1;
+        float f[GB];
+#pragma unroll
+        for (int h = 0; h < GB; ++h) {
+            s[h] += __shfl_xor_sync(0xffffffffu, s[h], 16);
+            s[h] = ok ? s[h] * scale2 : -CUDART_INF_F;
+            float mx = s[h];
+#pragma unroll
+            for (int d = 1; d < 16; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+            const float mn = fmaxf(m[h], mx);
+            f[h] = m[h] == mn ? 1.f : ex2(m[h] - mn);
+            m[h] = mn;
+            const float p = s[h] == -CUDART_INF_F ? 0.f : ex2(s[h] - mn);
+            l[h] = l[h] * f[h] + (half == 0 ? p : 0.f);  // each token counts once over the warp
+            if (half == 0) ps[t * GB + h] = p;
+#pragma unroll
+            for (int c = 0; c < NC; ++c) o[h][c] *= f[h];
+        }
+        __syncwarp();
+        const char *v = base + P::HALF;
+#pragma unroll 4
+        for (int u = 0; u < TILE; ++u) {
+            float x[NC];
+            const char *at = v + P::at(u, lane * NC / 4) + (lane * NC % 4) * 4;
+            if (NC == 4) {
+                const float4 y = *reinterpret_cast<const float4 *>(at);
+                x[0] = y.x; x[1] = y.y; x[NC - 2] = y.z; x[NC - 1] = y.w;
+            } else {
+                const float2 y = *reinterpret_cast<const float2 *>(at);
+                x[0] = y.x; x[1] = y.y;
+            }
+#pragma unroll
+            for (int h = 0; h < GB; ++h) {
+                const float p = ps[u * GB + h];
+#pragma unroll
+                for (int c = 0; c < NC; ++c) o[h][c] += p * x[c];
+            }
+        }
+        __syncwarp();  // ps is free for the next tile
+    }
+    __device__ __forceinline__ void finish() {
+#pragma unroll
+        for (int h = 0; h < GB; ++h) l[h] = warp_sum(l[h]);
+    }
+    static constexpr int HEADS = GB, VALS = GB * NC;
+    static __device__ __forceinline__ int head_of(int i) { return i; }
+    __device__ __forceinline__ float &mm(int i) { return m[i]; }
+    __device__ __forceinline__ float &ll(int i) { return l[i]; }
+    template <typename F> __device__ __forceinline__ void each(F f) {
+        const int lane = threadIdx.x & 31;
+#pragma unroll
+        for (int h = 0; h < GB; ++h)
+#pragma unroll
+            for (int c = 0; c < NC; ++c) f(h, h, lane * NC + c, o[h][c]);
+    }
+};
+
+template <class C, int D> constexpr int warp_bytes() { return C::STAGES * C::P::STAGE + C::EXTRA; }
+template <class C, int D> constexpr int smem_bytes() { return WARPS * warp_bytes<C, D>(); }
+
+template <class C, int D> __global__ void __launch_bounds__(THREADS) k_attn(const Args x) {
+    typedef typename C::E E;
+    typedef typename C::P P;
+    constexpr int GB = C::GB, STAGES = C::STAGES;
+    extern __shared__ __align__(128) char smem[];
+    __shared__ float sm_m[WARPS][GB], sm_l[WARPS][GB];
+    __shared__ float sm_o[GB][D + 1];
+    const AttnDecode &a = x.a;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int segs = a.Hk * x.RB;
+    const Run run = find_run(x, segs);
+    if (run.a0 >= run.a1) {
+        if (tid == 0) x.head[blockIdx.x] = make_int4(-1, 0, 0, 0);
+        // requests that see nothing, shared out over the CTAs below
+    }
+    for (int r = blockIdx.x; r < a.R; r += gridDim.x) {
+        Span sp;
+        sp.set(a, r);
+        if (sp.tiles > 0) continue;
+        for (int i = tid; i < a.Hq * D; i += THREADS) ((E *)a.out)[(size_t)r * a.Hq * D + i] = from_f<E>(0.f);
+        if (a.lse)
+            for (int i = tid; i < a.Hq; i += THREADS) a.lse[(size_t)r * a.Hq + i] = -CUDART_INF_F;
+    }
+    if (run.a0 >= run.a1) return;
+
+    char *mine = smem + warp * warp_bytes<C, D>();
+    const uint32_t stages = smem_u32(mine);
+    // the place of the run's first tile
+    Place here;
+    here.r = run.r0;
+    here.sp.set(a, here.r);
+    long long in = run.a0 - run.base;
+    here.seg = (int)(in / here.sp.tiles);
+    here.tile = (int)(in - (long long)here.seg * here.sp.tiles);
+
+    // the warp's loads run STAGES - 1 tiles ahead of its arithmetic
+    const int count = (int)(run.a1 - run.a0);  // tiles of the CTA; warp w takes w, w + WARPS, ...
+    Place next = here;
+    int issued = warp;
+    if (issued < count) advance(next, warp, segs, a);
+    int put = 0, got = 0;
+    __shared__ uint32_t lives[WARPS][STAGES];
+    auto issue = [&]() {
+        if (issued < count) {
+            const uint32_t bits = P::load(stages + put * P::STAGE, x, next);
+            if (lane == 0) lives[warp][put] = bits;
+            issued += WARPS;
+            if (issued < count) advance(next, WARPS, segs, a);
+        }
+        cp_commit();
+        put = put + 1 == STAGES ? 0 : put + 1;
+    };
+#pragma unroll
+    for (int i = 0; i < STAGES - 1; ++i) issue();
+
+    C c;
+    if constexpr (C::EXTRA > 0) {
+        c.qs = reinterpret_cast<float *>(mine + STAGES * P::STAGE);
+        c.ps = c.qs + GB * D;
+    }
+    int done = 0;  // tiles of the CTA's run before the current segment
+    int mytile = warp;
+    for (int part = 0; done < count; ++part) {
+        const int h = here.seg / x.RB, rb = here.seg - h * x.RB, head0 = h * x.G + rb * GB;
+        const int heads = min(GB, x.G - rb * GB);
+        const int upto = min(count, done + here.sp.tiles - here.tile);  // the segment's tiles in this run end here
+        c.start((const E *)a.q + ((size_t)here.r * a.Hq + head0) * D, heads);
+        for (; mytile < upto; mytile += WARPS) {
+            cp_wait<STAGES - 2>();
+            __syncwarp();
+            const uint32_t bits = lives[warp][got];
+            issue();
+            c.tile(stages + got * P::STAGE, bits, x.scale2, mine + got * P::STAGE);
+            got = got + 1 == STAGES ? 0 : got + 1;
+            __syncwarp();
+        }
+        c.finish();
+        // join the warps
+        __syncthreads();  // the join of the segment before is read
+#pragma unroll
+        for (int i = 0; i < C::HEADS; ++i) {
+            sm_m[warp][C::head_of(i)] = c.mm(i);
+            sm_l[warp][C::head_of(i)] = c.ll(i);
+        }
+        __syncthreads();
+        float f[C::HEADS], mj[C::HEADS], lj[C::HEADS];
+#pragma unroll
+        for (int i = 0; i < C::HEADS; ++i) {
+            const int hd = C::head_of(i);
+            float mx = sm_m[0][hd];
+#pragma unroll
+            for (int w = 1; w < WARPS; ++w) mx = fmaxf(mx, sm_m[w][hd]);
+            float s = 0.f;
+#pragma unroll
+            for (int w = 0; w < WARPS; ++w) s += part_of(sm_l[w][hd], sm_m[w][hd], mx);
+            f[i] = c.ll(i) == 0.f ? 0.f : ex2(c.mm(i) - mx);
+            mj[i] = mx;
+            lj[i] = s;
+        }
+        for (int w = 0; w < WARPS; ++w) {
+            if (warp == w)
+                c.each([&](int i, int hd, int ch, float o) {
+                    const float y = o * f[i];
+                    sm_o[hd][ch] = w == 0 ? y : sm_o[hd][ch] + y;
+                });
+            __syncthreads();
+        }
+        const bool begins = here.tile == 0, ends = done + here.sp.tiles - here.tile <= count;
+        if (begins && ends) {
+            E *dst = (E *)a.out + ((size_t)here.r * a.Hq + head0) * D;
+            for (int i = tid; i < heads * D; i += THREADS) {
+                const int hd = i / D;
+                float mx = sm_m[0][hd], s = 0.f;
+                for (int w = 1; w < WARPS; ++w) mx = fmaxf(mx, sm_m[w][hd]);
+                for (int w = 0; w < WARPS; ++w) s += part_of(sm_l[w][hd], sm_m[w][hd], mx);
+                dst[i] = from_f<E>(s > 0.f ? sm_o[hd][i - hd * D] / s : (s == s ? 0.f : s));
+                if (a.lse && i % D == 0)
+                    a.lse[(size_t)here.r * a.Hq + head0 + hd] = s > 0.f ? (mx + log2f(s)) * LN2 : (s == s ? -CUDART_INF_F : s);
+            }
+        } else {
+            float *dst = x.part + (size_t)(2 * blockIdx.x + (part > 0)) * GB * (D + 2);
+            for (int i = tid; i < GB * D; i += THREADS) dst[i / D * (D + 2) + i % D] = sm_o[i / D][i % D];
+            if (warp == 0)
+#pragma unroll
+                for (int i = 0; i < C::HEADS; ++i) {
+                    dst[C::head_of(i) * (D + 2) + D] = mj[i];
+                    dst[C::head_of(i) * (D + 2) + D + 1] = lj[i];
+                }
+        }
+        const int here_left = done + here.sp.tiles - here.tile;
+        if (tid == 0 && here_left >= count) {  // the run's last segment
+            int last = -1;
+            if (begins && !ends) {
+                const long long end = run.a0 + done + here.sp.tiles;  // the list's index behind the segment
+                last = (int)((end - 1) / run.per);
+            }
+            x.head[blockIdx.x] = last < 0 ? make_int4(-1, 0, 0, 0) : make_int4(here.r, h, rb | (part > 0) << 16, last);
+        }
+        done = upto;
+        if (done < count) {
+            here.tile = here.sp.tiles - 1;
+            advance(here, 1, segs, a);
+        }
+    }
+}
+
+// The split segment that begins in run blockIdx.x: one head (blockIdx.y), its parts added in order.
+template <typename E, int D> __global__ void __launch_bounds__(256) k_attn_join(const Args x) {
+    __shared__ float red[8][D], wm[8], wl[8];
+    const int4 hd = x.head[blockIdx.x];
+    if (hd.x < 0) return;
+    const int rb = hd.z & 0xffff, slot0 = hd.z >> 16, GB = x.GB, in = blockIdx.y, head = hd.y * x.G + rb * GB + in;
+    if (rb * GB + in >= x.G) return;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n = hd.w - (int)blockIdx.x + 1;
+    constexpr int NC = D / 32;
+    auto part = [&](int i) {  // part i: the CTA's second slot only for a segment that begins behind another
+        return x.part + ((size_t)(2 * (blockIdx.x + i) + (i == 0 ? slot0 : 0)) * GB + in) * (D + 2);
+    };
+    float m = -CUDART_INF_F;
+    for (int i = threadIdx.x; i < n; i += 256) m = fmaxf(m, part(i)[D]);
+    m = warp_max(m);
+    if (lane == 0) wm[warp] = m;
+    __syncthreads();
+    for (int w = 0; w < 8; ++w) m = fmaxf(m, wm[w]);
+    float o[NC] = {}, l = 0.f;
+#pragma unroll 4
+    for (int i = warp; i < n; i += 8) {
+        const float *p = part(i);
+        const float f = p[D + 1] == 0.f ? 0.f : ex2(p[D] - m);
+        l += p[D + 1] * f;
+#pragma unroll
+        for (int c = 0; c < NC; ++c) o[c] += f * p[c * 32 + lane];
+    }
+#pragma unroll
+    for (int c = 0; c < NC; ++c) red[warp][c * 32 + lane] = o[c];
+    if (lane == 0) wl[warp] = l;
+    __syncthreads();
+    l = 0.f;
+    for (int w = 0; w < 8; ++w) l += wl[w];
+    const size_t row = (size_t)hd.x * x.a.Hq + head;
+    for (int c = threadIdx.x; c < D; c += 256) {
+        float s = 0.f;
+        for (int w = 0; w < 8; ++w) s += red[w][c];
+        ((E *)x.a.out)[row * D + c] = from_f<E>(l > 0.f ? s / l : (l == l ? 0.f : l));
+    }
+    if (threadIdx.x == 0 && x.a.lse) x.a.lse[row] = l > 0.f ? (m + log2f(l)) * LN2 : (l == l ? -CUDART_INF_F : l);
+}
+
+template <class C, int D> static cudaError_t launch(Args x, cudaStream_t s) {
+    const AttnDecode &a = x.a;
+    x.GB = C::GB;
+    x.RB = (x.G + C::GB - 1) / C::GB;
+    x.head = (int4 *)a.ws;
+    x.part = (float *)((char *)a.ws + MAX_CTAS * sizeof(int4));
+    const int smem = smem_bytes<C, D>();
+    cudaError_t e = cudaFuncSetAttribute(k_attn<C, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    // no more CTAs than the tables have room for runs
+    const double tiles = (double)a.R * a.Hk * x.RB * ((double)a.width * a.page / TILE + 1);
+    const int ctas = tiles / MIN_TILES < C::CTAS - 1 ? (int)(tiles / MIN_TILES) + 1 : C::CTAS;
+    k_attn<C, D><<<ctas, THREADS, smem, s>>>(x);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    k_attn_join<typename C::E, D><<<dim3(ctas, x.G < C::GB ? x.G : C::GB), 256, 0, s>>>(x);
+    return cudaGetLastError();
+}
+
+static int heads_per_block(int G, bool bf16) { return !bf16 || G <= 8 ? 8 : 16; }
+
+}  // namespace ad
+
+size_t attn_decode_ws_bytes(int Hq, int Hk, int d, bool bf16) {
+    const int GB = ad::heads_per_block(Hq / Hk, bf16);
+    return ad::MAX_CTAS * sizeof(int4) + (size_t)2 * ad::MAX_CTAS * GB * (d + 2) * sizeof(float);
+}
+
+cudaError_t attn_decode_run(const AttnDecode &p, bool bf16, cudaStream_t s) {
+    ad::Args x = {};
+    x.a = p;
+    x.G = p.Hq / p.Hk;
+    x.scale2 = p.scale * ad::LOG2E;
+    const int GB = ad::heads_per_block(x.G, bf16);
+    if (!bf16) return p.d == 128 ? ad::launch<ad::Simt<128>, 128>(x, s) : ad::launch<ad::Simt<64>, 64>(x, s);
+    if (p.d == 128)
+        return GB == 8 ? ad::launch<ad::Mma<128, 1>, 128>(x, s) : ad::launch<ad::Mma<128, 2>, 128>(x, s);
+    return GB == 8 ? ad::launch<ad::Mma<64, 1>, 64>(x, s) : ad::launch<ad::Mma<64, 2>, 64>(x, s);
+}
+
+}  // namespace dr

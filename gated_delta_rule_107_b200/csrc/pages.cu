@@ -1,0 +1,142 @@
+// pages.cu -- pages of a key-value cache given to the requests of a batch, and each new token's
+// place in the cache, from the requests' lengths alone.
+//
+// Request r holds cached[r] tokens in have = ceil(cached / page) pages and gets fresh[r] more, so
+// need = ceil((cached + fresh) / page) pages.  With c, t the exclusive prefix sums over the
+// requests of fresh and of need - have:
+//   page j of request r, have <= j < need, is the (t[r] + j - have)th page from the top of the
+//     stack of free pages (-1 behind its end)
+//   token n, c[r] <= n < c[r + 1], has position p = cached[r] + n - c[r] and slot
+//     page(p / page) * page + p % page (-1 where that page is -1)
+//
+// One launch, and what a CTA writes depends on no other CTA: every CTA forms both prefix sums over
+// all requests for itself in shared memory (64 KB at the most requests; 509 requests take about a
+// microsecond), finds the request of a token or a page by bisection, and takes the page number of
+// a token from the table where the request had the page before and from the stack where it is
+// new.  So no CTA reads a table entry that another writes.  What bounds it is the launch and that
+// chain of dependent reads, not the bytes (12 a token).
+#include <limits.h>
+
+#include "pages.cuh"
+
+namespace dr {
+namespace pgs {
+
+constexpr int THREADS = 256;
+
+__device__ __forceinline__ int add_sat(int a, int b) {  // both >= 0; associative
+    const unsigned s = (unsigned)a + (unsigned)b;
+    return s > (unsigned)INT_MAX ? INT_MAX : (int)s;
+}
+// pages of n tokens, at most `width`
+__device__ __forceinline__ int pages_of(int n, int page, int width) {
+    return min(n / page + (n % page != 0), width);
+}
+// the last i in [0, R) with sum[i] <= x (sum[0] = 0 <= x)
+__device__ __forceinline__ int find(const int *sum, int R, int x) {
+    int lo = 0, hi = R;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (sum[mid] <= x) lo = mid; else hi = mid;
+    }
+    return lo;
+}
+
+__global__ void __launch_bounds__(THREADS) k_pages(const Pages p) {
+    extern __shared__ int sh[];
+    int *c = sh, *t = sh + p.R + 1;  // prefix sums [R + 1]: new tokens, new pages
+    __shared__ int wsum[2][THREADS / 32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    // each thread sums a run of requests, then the runs are scanned over the CTA
+    const int per = (p.R + THREADS - 1) / THREADS, r0 = min(p.R, tid * per), r1 = min(p.R, r0 + per);
+    int sc = 0, st = 0;
+    for (int r = r0; r < r1; ++r) {
+        const int a = max(p.cached[r], 0), f = max(p.fresh[r], 0);
+        c[r] = f;
+        t[r] = pages_of(add_sat(a, f), p.page, p.width) - pages_of(a, p.page, p.width);
+        sc = add_sat(sc, c[r]);
+        st = add_sat(st, t[r]);
+    }
+    int ic = sc, it = st;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int xc = __shfl_up_sync(0xffffffffu, ic, o), xt = __shfl_up_sync(0xffffffffu, it, o);
+        if (lane >= o) {
+            ic = add_sat(ic, xc);
+            it = add_sat(it, xt);
+        }
+    }
+    if (lane == 31) {
+        wsum[0][warp] = ic;
+        wsum[1][warp] = it;
+    }
+    // exclusive inside the warp: the inclusive sum of the lane before
+    int ec = __shfl_up_sync(0xffffffffu, ic, 1), et = __shfl_up_sync(0xffffffffu, it, 1);
+    if (lane == 0) ec = et = 0;
+    __syncthreads();
+    for (int w = 0; w < warp; ++w) {
+        ec = add_sat(ec, wsum[0][w]);
+        et = add_sat(et, wsum[1][w]);
+    }
+    for (int r = r0; r < r1; ++r) {
+        const int xc = c[r], xt = t[r];
+        c[r] = ec;
+        t[r] = et;
+        ec = add_sat(ec, xc);
+        et = add_sat(et, xt);
+    }
+    if ((r0 < p.R && r1 == p.R) || (p.R == 0 && tid == 0)) {
+        c[p.R] = ec;
+        t[p.R] = et;
+    }
+    __syncthreads();
+
+    const int total = c[p.R], taken = t[p.R], free = min(max(*p.n_free, 0), p.F);
+    // unsigned: an index below 2^31 plus a stride does not wrap
+    const unsigned gtid = blockIdx.x * THREADS + tid, gsize = gridDim.x * THREADS;
+    auto page_of = [&](int nth) { return nth < free ? p.free_pages[free - 1 - nth] : -1; };
+    for (unsigned r = gtid; r <= (unsigned)p.R; r += gsize) {
+        p.cu_new[r] = c[r];
+        if (r < (unsigned)p.R) p.lens[r] = add_sat(max(p.cached[r], 0), max(p.fresh[r], 0));
+    }
+    if (gtid == 0) *p.n_left = free - taken;
+    for (unsigned u = gtid; u < (unsigned)taken; u += gsize) {
+        const int i = (int)u, r = find(t, p.R, i);
+        const int j = pages_of(max(p.cached[r], 0), p.page, p.width) + i - t[r];
+        p.table[(size_t)r * p.width + j] = page_of(i);
+    }
+    for (unsigned u = gtid; u < (unsigned)p.N; u += gsize) {
+        const int n = (int)u;
+        int pos = 0;
+        long long slot = -1;
+        if (n < total) {
+            const int r = find(c, p.R, n), a = max(p.cached[r], 0);
+            pos = add_sat(a, n - c[r]);
+            const int j = pos / p.page, have = pages_of(a, p.page, p.width);
+            if (j < p.width) {
+                const int pg = j < have ? p.table[(size_t)r * p.width + j] : page_of(t[r] + j - have);
+                if (pg >= 0) slot = (long long)pg * p.page + (pos - j * p.page);
+            }
+        }
+        p.positions[n] = pos;
+        p.slots[n] = slot;
+    }
+}
+
+}  // namespace pgs
+
+cudaError_t pages_run(const Pages &p, cudaStream_t s) {
+    const size_t smem = 2 * ((size_t)p.R + 1) * sizeof(int);
+    if (smem > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(pgs::k_pages, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+    }
+    // a thread per token up to two CTAs an SM; at least enough for the requests' own outputs
+    const long long work = p.N > p.R ? p.N : p.R;
+    long long ctas = (work + pgs::THREADS - 1) / pgs::THREADS;
+    ctas = ctas < 1 ? 1 : (ctas > 296 ? 296 : ctas);
+    pgs::k_pages<<<(unsigned)ctas, pgs::THREADS, smem, s>>>(p);
+    return cudaGetLastError();
+}
+
+}  // namespace dr

@@ -372,6 +372,109 @@ int delta_rule_clvr_bwd(const void *u, const void *W, const void *dh_out, void *
                         int dtype, void *workspace, size_t ws_bytes, void *stream);
 
 /*
+ * The softmax-attention layers of a hybrid stack (the ETH news page, section 三,
+ * and the explainer train stacks with one softmax layer in three beside the
+ * delta-rule layers): their query / key norm with the rotation by position, for
+ * training and for serving, and the paged key-value cache a decoding step needs
+ * where a delta-rule layer has its state.  d = 64 or 128 channels a head for
+ * queries, keys and values; Hq query heads share Hk key heads.  dtype as above.
+ *
+ * Cache: keys and values in n_pages pages of `page` tokens each,
+ *     k_cache, v_cache  [n_pages][page][Hk][d],
+ * dense inside a page, consecutive pages k_page_stride / v_page_stride elements
+ * apart (>= page * Hk * d, a multiple of 16 bytes: both may lie in one buffer).
+ * A request's tokens are found through its row of the block table
+ * table [R][width] (int32): token t is row t % page of page table[r][t / page].
+ * The slot of a token is its page's number * page + its row (int64).
+ *
+ * delta_rule_pages: one step's bookkeeping for R <= 8192 requests, on the device
+ * and from lengths on the device (nothing is read back, so a captured step can
+ * be replayed).  cached [R] tokens are in the cache, fresh [R] are to be added
+ * (negative lengths count as 0).  The pages that the fresh tokens need beyond
+ * those of the cached ones are taken from the stack free_pages [F], whose top is
+ * entry *n_free - 1 (n_free is clamped to [0, F]), request by request, and
+ * written to the table behind the request's ceil(cached / page) entries; the
+ * other entries stay as they were.  Written besides:
+ *     lens [R]       cached + fresh
+ *     cu_new [R + 1] exclusive prefix sums of fresh: request r's tokens are
+ *                    rows cu_new[r] .. cu_new[r + 1] - 1 of the step's batch
+ *     positions [N]  each row's position (0 behind the last token)
+ *     slots [N]      each row's slot (-1 behind the last token)
+ *     n_left [1]     *n_free - the pages taken; negative: so many were missing
+ * N is the batch's capacity; tokens behind it get no row.  Where the stack ran
+ * short the table entry and the slots are -1; likewise the slots of tokens
+ * behind the table's width (no page is taken for those).  N <= 2^30.  n_left
+ * must not be n_free itself; the stack's entries are not changed, so the next
+ * step passes n_left as its n_free.
+ */
+int delta_rule_pages(const int *cached, const int *fresh, const int *free_pages, const int *n_free, int *table,
+                     int *lens, int *cu_new, int *positions, long long *slots, int *n_left, int R, int F, int width,
+                     int page, int N, void *stream);
+
+/*
+ * Norm of each query and key head, and rotation by position, one pass over
+ * memory.  For every row x of d channels, eps = 1e-6,
+ *     y = x / sqrt(mean(x^2) + eps) * w,
+ * then the first rot channels in pairs, (a, b) -> (a cos - b sin, b cos + a sin)
+ * with the angle position * inv_freq[i] for pair i = 0 .. rot/2 - 1: channels
+ * (i, i + rot/2), or (2i, 2i + 1) when interleaved = 1.  rot is a multiple of 16
+ * up to d; 0 rotates nothing.  wq, wk are fp32 [d] (NULL = all ones), inv_freq is
+ * fp64 [rot/2], positions int32 [B*T] (NULL: the token's index t in its
+ * sequence); the angle is formed in 64 bits, so far positions keep their
+ * precision.  q [B,T,Hq,d] and k [B,T,Hk,d] may be slices of one projection:
+ * q_stride, k_stride are the elements from a token to the next (>= heads * d, a
+ * multiple of 16 bytes), a token's heads are dense.  q_out, k_out are dense.
+ * Hq or Hk may be 0 (its pointers are then unused); Hq + Hk <= 1024.
+ *
+ * delta_rule_qkrope_bwd: for dq_out, dk_out (dense), the gradients dq, dk_ of q
+ * and k (token strides dq_stride, dk_stride) and dwq, dwk [d] fp32, the sums
+ * over all rows (NULL = not written; otherwise a workspace of
+ * delta_rule_qkrope_workspace_size(d) bytes, 256-byte aligned).  They are summed
+ * in a fixed order, so results are deterministic.
+ *
+ * delta_rule_qkrope_cache: the serving form for N tokens of any requests.  The
+ * queries go to q_out [N,Hq,d]; the keys, normed and rotated, and the values
+ * v [N,Hk,d] (token stride v_stride), as they are, into the cache rows
+ * slots[n].  A token whose slot is outside [0, n_pages * page) is padding:
+ * nothing of the cache is written for it (q_out is).  The slots of the others
+ * must differ: which of two tokens of one slot the row keeps is not defined.
+ */
+int delta_rule_qkrope(const void *q, const void *k, const float *wq, const float *wk, const double *inv_freq,
+                      const int *positions, void *q_out, void *k_out, int B, int T, int Hq, int Hk, int d, int rot,
+                      int interleaved, long long q_stride, long long k_stride, int dtype, void *stream);
+size_t delta_rule_qkrope_workspace_size(int d);
+int delta_rule_qkrope_bwd(const void *q, const void *k, const float *wq, const float *wk, const double *inv_freq,
+                          const int *positions, const void *dq_out, const void *dk_out, void *dq, void *dk_,
+                          float *dwq, float *dwk, int B, int T, int Hq, int Hk, int d, int rot, int interleaved,
+                          long long q_stride, long long k_stride, long long dq_stride, long long dk_stride,
+                          int dtype, void *workspace, size_t ws_bytes, void *stream);
+int delta_rule_qkrope_cache(const void *q, const void *k, const void *v, const float *wq, const float *wk,
+                            const double *inv_freq, const int *positions, const long long *slots, void *q_out,
+                            void *k_cache, void *v_cache, int N, int Hq, int Hk, int d, int rot, int interleaved,
+                            long long q_stride, long long k_stride, long long v_stride, int n_pages, int page,
+                            long long k_page_stride, long long v_page_stride, int dtype, void *stream);
+
+/*
+ * Attention of one new token per request over the paged cache.  q [R,Hq,d] is
+ * request r's query, lens[r] its cached tokens (the new token's own key and value
+ * among them), and h's group of Hq / Hk query heads shares key head h / (Hq / Hk):
+ *     s_t = scale q . k_t  over t in [max(0, lens[r] - window), lens[r])
+ *     out [R,Hq,d] = sum_t e^{s_t} v_t / sum_t e^{s_t},  lse [R,Hq] = log sum_t e^{s_t}
+ * (lse fp32, NULL = not written; window = 0: all tokens).  A request that sees no
+ * token gets out = 0, lse = -inf.  Tokens behind the table's width, and tokens
+ * whose table entry is no page (outside [0, n_pages)), are not seen; what their
+ * rows hold is not read.  Sums and softmax statistics are fp32.  Results do not
+ * change from run to run.  The workspace is
+ * delta_rule_attn_decode_workspace_size(Hq, Hk, d, dtype) bytes (whatever the
+ * lengths; (size_t)-1 for invalid arguments), 256-byte aligned.
+ */
+size_t delta_rule_attn_decode_workspace_size(int Hq, int Hk, int d, int dtype);
+int delta_rule_attn_decode(const void *q, const void *k_cache, const void *v_cache, const int *table,
+                           const int *lens, void *out, float *lse, int R, int Hq, int Hk, int d, int n_pages,
+                           int page, int width, long long k_page_stride, long long v_page_stride, float scale,
+                           int window, int dtype, void *workspace, size_t ws_bytes, void *stream);
+
+/*
  * Self-test of failure detection.  Launches one kernel on `stream` whose bounded
  * wait (the same wait every pipelined kernel uses) waits for a barrier phase that
  * nothing completes; after limit_us microseconds (1 .. 1,000,000) it gives up,
