@@ -26,8 +26,8 @@
 //     into two bf16 numbers (high and rest, 2^-17 of p) and multiplied twice: rounding P once
 //     would put as large an error in the output as its own rounding, and the second product is
 //     hidden behind the loads.
-//   fp32.  CUDA cores, up to 8 heads at a time: a lane holds half a token's channels for the
-//     scores, 1/32 of the channels of every head for the output.
+//   fp32.  CUDA cores, 1, 2, 4 or up to 8 heads at a time: a lane holds half a token's channels for
+//     the scores, 1/32 of the channels of every head for the output.
 // Tokens that are masked (or whose table entry is no page) are neither read nor seen: their rows
 // in shared memory are zero-filled, their scores -inf.  A request with none gives o = 0, lse = -inf.
 #include <math_constants.h>
@@ -49,6 +49,8 @@ struct Args {
     float *part;         // [2 * MAX_CTAS][GB][D + 2]: o (not divided by l), m, l
     int4 *head;          // [MAX_CTAS]: the split segment that begins in a CTA: request, key head, block, last CTA
     float scale2;
+    FastDiv by_page;
+    bool whole;          // a tile never crosses a page (the page is a multiple of the tile)
 };
 
 __device__ __forceinline__ uint32_t smem_u32(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
@@ -190,29 +192,54 @@ template <typename E, int D, int STAGES> struct Pipe {
     // eight rows at one chunk lie in eight different banks groups
     static __device__ __forceinline__ uint32_t at(int r, int c) { return r * ROW + ((c ^ (r & 7)) << 4); }
 
-    // copies the tile at pl into the stage; returns the bits of its live tokens
-    static __device__ __forceinline__ uint32_t load(uint32_t stage, const Args &x, const Place &pl) {
+    // What a tile's copies need: the lane's token (lane % 16) is row `in` of page pg (-1: not seen;
+    // read ahead of the copies, since the table is a read of its own), key head h.
+    struct Want {
+        int pg, in, h;
+    };
+    static __device__ __forceinline__ Want want(const Args &x, const Place &pl) {
         const AttnDecode &a = x.a;
-        const int lane = threadIdx.x & 31, h = pl.seg / x.RB;
-        const int t = (pl.sp.tile0 + pl.tile) * TILE + (lane & 15);
-        int pg = -1, in = 0;
+        const int t = (pl.sp.tile0 + pl.tile) * TILE + (threadIdx.x & 15);
+        Want w = {-1, 0, pl.seg / x.RB};
         if (t >= pl.sp.first && t < pl.sp.n) {
-            const int col = t / a.page;
-            in = t - col * a.page;
-            pg = a.table[(size_t)pl.r * a.width + col];
-            if (pg >= a.n_pages) pg = -1;
+            const int col = x.by_page.div(t);
+            const int *at = a.table + (size_t)pl.r * a.width + col;
+            w.in = t - col * a.page;
+            w.pg = *at;
+            // the entries that this CTA reads some tiles on
+            if ((threadIdx.x & 15) == 0 && col + AHEAD < a.width) asm volatile("prefetch.global.L2 [%0];" ::"l"(at + AHEAD));
         }
-        const uint32_t live = __ballot_sync(0xffffffffu, pg >= 0) & 0xffffu;
-        const int c = lane % CPR, row0 = lane / CPR;
-        const size_t inside = ((size_t)in * a.Hk + h) * D;
-        const size_t ko = pg < 0 ? 0 : (size_t)pg * a.kps + inside, vo = pg < 0 ? 0 : (size_t)pg * a.vps + inside;
+        return w;
+    }
+    static constexpr int AHEAD = 128;
+
+    // copies the tile into the stage; returns the bits of its live tokens
+    static __device__ __forceinline__ uint32_t load(uint32_t stage, const Args &x, const Want &w) {
+        const AttnDecode &a = x.a;
+        const int lane = threadIdx.x & 31;
+        const bool seen = w.pg >= 0 && w.pg < a.n_pages;
+        const uint32_t live = __ballot_sync(0xffffffffu, seen) & 0xffffu;
+        const int c = lane % CPR, row0 = lane / CPR, e16 = 16 / (int)sizeof(E);
+        const size_t inside = ((size_t)w.in * a.Hk + w.h) * D;
+        const size_t ko = seen ? (size_t)w.pg * a.kps + inside : 0, vo = seen ? (size_t)w.pg * a.vps + inside : 0;
+        if (x.whole && live == 0xffffu) {  // 16 rows of one page: evenly spaced from the first one's
+            const size_t apart = (size_t)a.Hk * D;
+            const E *k = (const E *)a.kc + __shfl_sync(0xffffffffu, ko, 0) + row0 * apart + c * e16;
+            const E *v = (const E *)a.vc + __shfl_sync(0xffffffffu, vo, 0) + row0 * apart + c * e16;
+#pragma unroll
+            for (int i = 0; i < TILE; i += RPI) {
+                cp16(stage + at(i + row0, c), k + i * apart, true);
+                cp16(stage + HALF + at(i + row0, c), v + i * apart, true);
+            }
+            return live;
+        }
 #pragma unroll
         for (int i = 0; i < TILE; i += RPI) {
             const int row = i + row0;
             const size_t k = __shfl_sync(0xffffffffu, ko, row), v = __shfl_sync(0xffffffffu, vo, row);
             const bool ok = live >> row & 1;
-            cp16(stage + at(row, c), (const E *)a.kc + k + c * (16 / (int)sizeof(E)), ok);
-            cp16(stage + HALF + at(row, c), (const E *)a.vc + v + c * (16 / (int)sizeof(E)), ok);
+            cp16(stage + at(row, c), (const E *)a.kc + k + c * e16, ok);
+            cp16(stage + HALF + at(row, c), (const E *)a.vc + v + c * e16, ok);
         }
         return live;
     }
@@ -369,9 +396,9 @@ template <int D, int NT> struct Mma {  // bf16: blocks of 8 NT heads
     static constexpr int EXTRA = 0;  // bytes of shared memory of the warp's own
 };
 
-template <int D> struct Simt {  // fp32: blocks of 8 heads
+template <int D, int H> struct Simt {  // fp32: blocks of H heads, at most 8
     typedef float E;
-    static constexpr int GB = 8, STAGES = (D == 128 ? 3 : 6), CTAS = MAX_CTAS / 2, NC = D / 32;
+    static constexpr int GB = H, STAGES = 3, CTAS = D == 128 ? MAX_CTAS / 2 : MAX_CTAS, NC = D / 32;
     typedef Pipe<E, D, STAGES> P;
     float o[GB][NC], m[GB], l[GB];
     static constexpr int EXTRA = (GB * D + TILE * GB) * 4;  // the block's queries, the tile's p
@@ -476,6 +503,7 @@ template <class C, int D> __global__ void __launch_bounds__(THREADS) k_attn(cons
     const AttnDecode &a = x.a;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int segs = a.Hk * x.RB;
+    asm volatile("griddepcontrol.launch_dependents;");  // the join may take its places; it waits for this kernel's end
     const Run run = find_run(x, segs);
     if (run.a0 >= run.a1) {
         if (tid == 0) x.head[blockIdx.x] = make_int4(-1, 0, 0, 0);
@@ -501,25 +529,37 @@ template <class C, int D> __global__ void __launch_bounds__(THREADS) k_attn(cons
     here.seg = (int)(in / here.sp.tiles);
     here.tile = (int)(in - (long long)here.seg * here.sp.tiles);
 
-    // the warp's loads run STAGES - 1 tiles ahead of its arithmetic
+    // the warp's loads run STAGES - 1 tiles ahead of its arithmetic, the table's entries one more
     const int count = (int)(run.a1 - run.a0);  // tiles of the CTA; warp w takes w, w + WARPS, ...
-    Place next = here;
-    int issued = warp;
-    if (issued < count) advance(next, warp, segs, a);
-    int put = 0, got = 0;
     __shared__ uint32_t lives[WARPS][STAGES];
-    auto issue = [&]() {
-        if (issued < count) {
-            const uint32_t bits = P::load(stages + put * P::STAGE, x, next);
-            if (lane == 0) lives[warp][put] = bits;
-            issued += WARPS;
-            if (issued < count) advance(next, WARPS, segs, a);
+    Place next = here;
+    typename P::Want ahead[STAGES] = {};
+    int known = warp;  // the tile that `next` is at
+    if (known < count) {
+        advance(next, warp, segs, a);
+        ahead[0] = P::want(x, next);
+    }
+#pragma unroll
+    for (int i = 1; i < STAGES; ++i) {
+        known += WARPS;
+        if (known < count) {
+            advance(next, WARPS, segs, a);
+            ahead[i] = P::want(x, next);
         }
+    }
+    int put = 0, got = 0, issued = warp;
+    auto issue = [&](const typename P::Want &w) {
+        if (issued < count) {
+            const uint32_t bits = P::load(stages + put * P::STAGE, x, w);
+            if (lane == 0) lives[warp][put] = bits;
+        }
+        issued += WARPS;
         cp_commit();
         put = put + 1 == STAGES ? 0 : put + 1;
     };
 #pragma unroll
-    for (int i = 0; i < STAGES - 1; ++i) issue();
+    for (int i = 0; i < STAGES - 1; ++i) issue(ahead[i]);
+    typename P::Want coming = ahead[STAGES - 1];
 
     C c;
     if constexpr (C::EXTRA > 0) {
@@ -537,7 +577,12 @@ template <class C, int D> __global__ void __launch_bounds__(THREADS) k_attn(cons
             cp_wait<STAGES - 2>();
             __syncwarp();
             const uint32_t bits = lives[warp][got];
-            issue();
+            issue(coming);
+            known += WARPS;
+            if (known < count) {
+                advance(next, WARPS, segs, a);
+                coming = P::want(x, next);
+            }
             c.tile(stages + got * P::STAGE, bits, x.scale2, mine + got * P::STAGE);
             got = got + 1 == STAGES ? 0 : got + 1;
             __syncwarp();
@@ -615,6 +660,7 @@ template <class C, int D> __global__ void __launch_bounds__(THREADS) k_attn(cons
 // The split segment that begins in run blockIdx.x: one head (blockIdx.y), its parts added in order.
 template <typename E, int D> __global__ void __launch_bounds__(256) k_attn_join(const Args x) {
     __shared__ float red[8][D], wm[8], wl[8];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int4 hd = x.head[blockIdx.x];
     if (hd.x < 0) return;
     const int rb = hd.z & 0xffff, slot0 = hd.z >> 16, GB = x.GB, in = blockIdx.y, head = hd.y * x.G + rb * GB + in;
@@ -669,11 +715,28 @@ template <class C, int D> static cudaError_t launch(Args x, cudaStream_t s) {
     k_attn<C, D><<<ctas, THREADS, smem, s>>>(x);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    k_attn_join<typename C::E, D><<<dim3(ctas, x.G < C::GB ? x.G : C::GB), 256, 0, s>>>(x);
-    return cudaGetLastError();
+    // launched while k_attn runs, so that only its work follows (2 us less on the smallest calls)
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3(ctas, x.G < C::GB ? x.G : C::GB);
+    cfg.blockDim = dim3(256);
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k_attn_join<typename C::E, D>, x);
 }
 
-static int heads_per_block(int G, bool bf16) { return !bf16 || G <= 8 ? 8 : 16; }
+static int heads_per_block(int G, bool bf16) {
+    if (bf16) return G <= 8 ? 8 : 16;
+    return G <= 2 ? G : (G <= 4 ? 4 : 8);
+}
+
+template <int D> static cudaError_t simt(const Args &x, int GB, cudaStream_t s) {
+    return GB == 1 ? launch<Simt<D, 1>, D>(x, s)
+                   : (GB == 2 ? launch<Simt<D, 2>, D>(x, s) : (GB == 4 ? launch<Simt<D, 4>, D>(x, s) : launch<Simt<D, 8>, D>(x, s)));
+}
 
 }  // namespace ad
 
@@ -687,8 +750,10 @@ cudaError_t attn_decode_run(const AttnDecode &p, bool bf16, cudaStream_t s) {
     x.a = p;
     x.G = p.Hq / p.Hk;
     x.scale2 = p.scale * ad::LOG2E;
+    x.by_page = FastDiv(p.page);
+    x.whole = p.page % ad::TILE == 0;
     const int GB = ad::heads_per_block(x.G, bf16);
-    if (!bf16) return p.d == 128 ? ad::launch<ad::Simt<128>, 128>(x, s) : ad::launch<ad::Simt<64>, 64>(x, s);
+    if (!bf16) return p.d == 128 ? ad::simt<128>(x, GB, s) : ad::simt<64>(x, GB, s);
     if (p.d == 128)
         return GB == 8 ? ad::launch<ad::Mma<128, 1>, 128>(x, s) : ad::launch<ad::Mma<128, 2>, 128>(x, s);
     return GB == 8 ? ad::launch<ad::Mma<64, 1>, 64>(x, s) : ad::launch<ad::Mma<64, 2>, 64>(x, s);

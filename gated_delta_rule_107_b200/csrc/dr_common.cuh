@@ -33,6 +33,20 @@ __device__ __forceinline__ float warp_max(float x) {
     return x;
 }
 
+// n / d for 0 <= n < 2^31, d >= 1, by a product: with 2^(s-1) < d <= 2^s and m = ceil(2^(31+s) / d)
+// (32 bits), m d exceeds 2^(31+s) by less than d <= 2^s, so n m / 2^(31+s) exceeds n / d by less than
+// 1 / d and has the same whole part.
+struct FastDiv {
+    uint32_t m;
+    int s, d;
+    FastDiv() = default;
+    explicit FastDiv(int by) : s(0), d(by) {
+        while (s < 31 && (1u << s) < (uint32_t)by) ++s;
+        m = (uint32_t)(((1ull << (31 + s)) + (uint64_t)by - 1) / (uint64_t)by);
+    }
+    __device__ __forceinline__ int div(int n) const { return (int)(((uint64_t)(uint32_t)n * m) >> (31 + s)); }
+};
+
 // Problem geometry shared by all kernels.  N = number of chunks = ceil(T / C).
 struct Geo {
     int B, T, H, dk, dv, C, N, variant;

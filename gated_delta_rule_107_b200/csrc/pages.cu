@@ -22,15 +22,17 @@
 namespace dr {
 namespace pgs {
 
-constexpr int THREADS = 256;
+constexpr int THREADS = 1024, MAX_CTAS = 148;
+constexpr int UNROLL = 4;  // tokens of a thread, side by side: their bisections and reads overlap
 
 __device__ __forceinline__ int add_sat(int a, int b) {  // both >= 0; associative
     const unsigned s = (unsigned)a + (unsigned)b;
     return s > (unsigned)INT_MAX ? INT_MAX : (int)s;
 }
-// pages of n tokens, at most `width`
-__device__ __forceinline__ int pages_of(int n, int page, int width) {
-    return min(n / page + (n % page != 0), width);
+// pages of n tokens, at most the table's width
+__device__ __forceinline__ int pages_of(int n, const Pages &p) {
+    const int q = p.by_page.div(n);
+    return min(q + (n != q * p.page), p.width);
 }
 // the last i in [0, R) with sum[i] <= x (sum[0] = 0 <= x)
 __device__ __forceinline__ int find(const int *sum, int R, int x) {
@@ -53,7 +55,7 @@ __global__ void __launch_bounds__(THREADS) k_pages(const Pages p) {
     for (int r = r0; r < r1; ++r) {
         const int a = max(p.cached[r], 0), f = max(p.fresh[r], 0);
         c[r] = f;
-        t[r] = pages_of(add_sat(a, f), p.page, p.width) - pages_of(a, p.page, p.width);
+        t[r] = pages_of(add_sat(a, f), p) - pages_of(a, p);
         sc = add_sat(sc, c[r]);
         st = add_sat(st, t[r]);
     }
@@ -102,39 +104,52 @@ __global__ void __launch_bounds__(THREADS) k_pages(const Pages p) {
     if (gtid == 0) *p.n_left = free - taken;
     for (unsigned u = gtid; u < (unsigned)taken; u += gsize) {
         const int i = (int)u, r = find(t, p.R, i);
-        const int j = pages_of(max(p.cached[r], 0), p.page, p.width) + i - t[r];
+        const int j = pages_of(max(p.cached[r], 0), p) + i - t[r];
         p.table[(size_t)r * p.width + j] = page_of(i);
     }
-    for (unsigned u = gtid; u < (unsigned)p.N; u += gsize) {
-        const int n = (int)u;
-        int pos = 0;
-        long long slot = -1;
-        if (n < total) {
-            const int r = find(c, p.R, n), a = max(p.cached[r], 0);
-            pos = add_sat(a, n - c[r]);
-            const int j = pos / p.page, have = pages_of(a, p.page, p.width);
-            if (j < p.width) {
-                const int pg = j < have ? p.table[(size_t)r * p.width + j] : page_of(t[r] + j - have);
-                if (pg >= 0) slot = (long long)pg * p.page + (pos - j * p.page);
+    for (unsigned u = gtid; u < (unsigned)p.N; u += UNROLL * gsize) {
+        int r[UNROLL], pos[UNROLL], pg[UNROLL];
+#pragma unroll
+        for (int k = 0; k < UNROLL; ++k) {  // behind the last token: the last request, dropped below
+            const unsigned n = u + k * gsize;
+            r[k] = total > 0 ? find(c, p.R, n < (unsigned)total ? (int)n : total - 1) : 0;
+        }
+#pragma unroll
+        for (int k = 0; k < UNROLL; ++k) {
+            const unsigned n = u + k * gsize;
+            pos[k] = 0;
+            pg[k] = -1;
+            if (n < (unsigned)total && n < (unsigned)p.N) {
+                const int a = max(p.cached[r[k]], 0);
+                pos[k] = add_sat(a, (int)n - c[r[k]]);
+                const int j = p.by_page.div(pos[k]), have = pages_of(a, p);
+                if (j < p.width) pg[k] = j < have ? p.table[(size_t)r[k] * p.width + j] : page_of(t[r[k]] + j - have);
             }
         }
-        p.positions[n] = pos;
-        p.slots[n] = slot;
+#pragma unroll
+        for (int k = 0; k < UNROLL; ++k) {
+            const unsigned n = u + k * gsize;
+            if (n >= (unsigned)p.N) break;
+            p.positions[n] = pos[k];
+            p.slots[n] = pg[k] < 0 ? -1ll : (long long)pg[k] * p.page + (pos[k] - p.by_page.div(pos[k]) * p.page);
+        }
     }
 }
 
 }  // namespace pgs
 
-cudaError_t pages_run(const Pages &p, cudaStream_t s) {
+cudaError_t pages_run(const Pages &args, cudaStream_t s) {
+    Pages p = args;
+    p.by_page = FastDiv(p.page);
     const size_t smem = 2 * ((size_t)p.R + 1) * sizeof(int);
     if (smem > 48 * 1024) {
         const cudaError_t e = cudaFuncSetAttribute(pgs::k_pages, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
     }
-    // a thread per token up to two CTAs an SM; at least enough for the requests' own outputs
+    // a thread per token up to one CTA an SM, and at least enough for the requests' own outputs
     const long long work = p.N > p.R ? p.N : p.R;
     long long ctas = (work + pgs::THREADS - 1) / pgs::THREADS;
-    ctas = ctas < 1 ? 1 : (ctas > 296 ? 296 : ctas);
+    ctas = ctas < 1 ? 1 : (ctas > pgs::MAX_CTAS ? pgs::MAX_CTAS : ctas);
     pgs::k_pages<<<(unsigned)ctas, pgs::THREADS, smem, s>>>(p);
     return cudaGetLastError();
 }

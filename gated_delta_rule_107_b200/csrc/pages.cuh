@@ -13,6 +13,7 @@ struct Pages {
     int *lens, *cu_new, *positions, *n_left;
     long long *slots;
     int R, F, width, page, N;
+    FastDiv by_page;  // set by pages_run
 };
 cudaError_t pages_run(const Pages &p, cudaStream_t s);
 
