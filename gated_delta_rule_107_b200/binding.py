@@ -30,6 +30,7 @@ The ``for_bwd`` argument of ``workspace_size`` and ``launches`` names the call:
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 
@@ -609,23 +610,27 @@ def attn_decode_raw(*args) -> int:
     return load().delta_rule_attn_decode(*args)
 
 
+def _refuse(t, what, dtype, dev, shape):
+    if t.dtype is not dtype or t.device != dev:
+        raise ValueError(f"{what}: expected {dtype} on {dev}, got {t.dtype} on {t.device}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{what}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    raise ValueError(f"{what} must be contiguous")
+
+
 def _arg(t, what, dtype, dev, shape=None):
     """Address of a dense tensor argument of the given element type, device and shape; None stays None."""
     if t is None:
         return None
-    if t.dtype != dtype or t.device != dev:
-        raise ValueError(f"{what}: expected {dtype} on {dev}, got {t.dtype} on {t.device}")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{what}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{what} must be contiguous")
+    if t.dtype is not dtype or t.device != dev or (shape is not None and t.shape != shape) or not t.is_contiguous():
+        _refuse(t, what, dtype, dev, shape)
     return t.data_ptr()
 
 
 def _token_stride(t, what, dtype, dev):
     """Elements from a token to the next of a [B, T, H, d] or [N, H, d] tensor with dense heads."""
-    if t.dtype != dtype or t.device != dev:
-        raise ValueError(f"{what}: expected {dtype} on {dev}, got {t.dtype} on {t.device}")
+    if t.dtype is not dtype or t.device != dev:
+        _refuse(t, what, dtype, dev, None)
     shape, st = t.shape, t.stride()
     ok = len(shape) in (3, 4)
     if ok:
@@ -652,15 +657,26 @@ def _cuda(t, what):
     return dev
 
 
+# The current stream's handle.  torch.cuda.current_stream() builds a Stream object first, which takes
+# about as long (3 us) as the rest of a small call's arguments together.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _launch(fn, what, dev, *args):
     """Calls a C entry point on the tensors' device and that device's current stream (the last argument)."""
-    if torch.cuda.current_device() == dev.index:
-        rc = fn(*args, torch.cuda.current_stream().cuda_stream)
+    index = dev.index
+    if torch.cuda.current_device() == index:
+        rc = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(dev):
-            rc = fn(*args, torch.cuda.current_stream().cuda_stream)
+            rc = fn(*args, _raw_stream(index))
     if rc != DR_OK:
         raise DeltaRuleError(rc, what)
+
+
+def _dense_like(t):
+    return torch.empty_like(t, memory_format=torch.contiguous_format)
 
 
 def delta_rule_pages(cached, fresh, free_pages, n_free, table, page, tokens):
@@ -680,7 +696,7 @@ def delta_rule_pages(cached, fresh, free_pages, n_free, table, page, tokens):
     if table.shape[0] != R or tokens < 0:
         raise ValueError(f"table: expected {R} rows, got {table.shape[0]} (tokens {tokens})")
     ints = torch.empty(2 * R + 2 + tokens, dtype=i32, device=dev)
-    lens, cu_new, n_left, positions = ints[:R], ints[R:2 * R + 1], ints[2 * R + 1:2 * R + 2], ints[2 * R + 2:]
+    lens, cu_new, n_left, positions = ints.split((R, R + 1, 1, tokens))
     slots = torch.empty(tokens, dtype=torch.int64, device=dev)
     at = ints.data_ptr()
     _launch(load().delta_rule_pages, "delta_rule_pages", dev, _arg(cached, "cached", i32, dev),
@@ -717,11 +733,19 @@ def delta_rule_qkrope(q, k, wq=None, wk=None, inv_freq=None, positions=None, int
     fp32 [d] or None; inv_freq fp64 [rot / 2] or None (no rotation); positions int32 [B, T] or None
     (0 .. T - 1); interleaved: channel pairs (2i, 2i + 1) instead of (i, i + rot / 2)."""
     dev, dt, B, T, d, rot, qs, ks, wqp, wkp, fp, pp_ = _qk(q, k, wq, wk, inv_freq, positions)
-    q_out, k_out = torch.empty(q.shape, dtype=dt, device=dev), torch.empty(k.shape, dtype=dt, device=dev)
+    q_out, k_out = _dense_like(q), _dense_like(k)
     _launch(load().delta_rule_qkrope, "delta_rule_qkrope", dev, q.data_ptr(), k.data_ptr(), wqp, wkp, fp, pp_,
             q_out.data_ptr(), k_out.data_ptr(), B, T, q.shape[-2], k.shape[-2], d, rot, int(interleaved), qs, ks,
             DTYPES[dt])
     return q_out, k_out
+
+
+@functools.lru_cache(maxsize=None)
+def qkrope_workspace_size(d) -> int:
+    n = load().delta_rule_qkrope_workspace_size(d)
+    if n == ctypes.c_size_t(-1).value:
+        raise DeltaRuleError(DR_ERR_UNSUPPORTED, "delta_rule_qkrope_workspace_size")
+    return n
 
 
 def delta_rule_qkrope_bwd(q, k, wq, wk, inv_freq, dq_out, dk_out, positions=None, interleaved=False, dq=None,
@@ -730,21 +754,23 @@ def delta_rule_qkrope_bwd(q, k, wq, wk, inv_freq, dq_out, dk_out, positions=None
     (None without want_dw).  dq, dk may be given: slices of one projection's gradient, say."""
     dev, dt, B, T, d, rot, qs, ks, wqp, wkp, fp, pp_ = _qk(q, k, wq, wk, inv_freq, positions)
     if dq is None:
-        dq = torch.empty(q.shape, dtype=dt, device=dev)
+        dq = _dense_like(q)
     if dk is None:
-        dk = torch.empty(k.shape, dtype=dt, device=dev)
+        dk = _dense_like(k)
     if dq.shape != q.shape or dk.shape != k.shape:
         raise ValueError("dq, dk must be shaped like q, k")
     dqs, dks = _token_stride(dq, "dq", dt, dev), _token_stride(dk, "dk", dt, dev)
-    dw = torch.empty((2, d), dtype=torch.float32, device=dev) if want_dw else None
-    need = load().delta_rule_qkrope_workspace_size(d) if want_dw else 0
-    ws = torch.empty(need, dtype=torch.uint8, device=dev) if 0 < need < 1 << 40 else None
-    at = dw.data_ptr() if want_dw else None
+    dwq = dwk = None
+    if want_dw:
+        dwq, dwk = (torch.empty(d, dtype=torch.float32, device=dev) if w is None else torch.empty_like(w)
+                    for w in (wq, wk))
+    need = qkrope_workspace_size(d) if want_dw else 0
+    ws = torch.empty(need, dtype=torch.uint8, device=dev) if want_dw else None
     _launch(load().delta_rule_qkrope_bwd, "delta_rule_qkrope_bwd", dev, q.data_ptr(), k.data_ptr(), wqp, wkp, fp, pp_,
             _arg(dq_out, "dq_out", dt, dev, q.shape), _arg(dk_out, "dk_out", dt, dev, k.shape), dq.data_ptr(),
-            dk.data_ptr(), at, at + 4 * d if want_dw else None, B, T, q.shape[-2], k.shape[-2], d, rot,
+            dk.data_ptr(), dwq.data_ptr() if want_dw else None, dwk.data_ptr() if want_dw else None, B, T, q.shape[-2], k.shape[-2], d, rot,
             int(interleaved), qs, ks, dqs, dks, DTYPES[dt], None if ws is None else ws.data_ptr(), need)
-    return (dq, dk, dw[0], dw[1]) if want_dw else (dq, dk, None, None)
+    return dq, dk, dwq, dwk
 
 
 def _page_stride(t, what, dtype, dev):
@@ -772,7 +798,7 @@ def delta_rule_qkrope_cache(q, k, v, wq, wk, inv_freq, positions, slots, k_cache
         raise ValueError(f"the caches must be [pages, page, {k.shape[-2]}, {d}], got {tuple(k_cache.shape)}, "
                          f"{tuple(v_cache.shape)}")
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=dt, device=dev)
+        q_out = _dense_like(q)
     _launch(load().delta_rule_qkrope_cache, "delta_rule_qkrope_cache", dev, q.data_ptr(), k.data_ptr(), v.data_ptr(),
             wqp, wkp, fp, pp_, _arg(slots, "slots", torch.int64, dev), _arg(q_out, "q_out", dt, dev, q.shape),
             k_cache.data_ptr(), v_cache.data_ptr(), B * T, q.shape[-2], k.shape[-2], d, rot, int(interleaved), qs, ks,
@@ -780,6 +806,7 @@ def delta_rule_qkrope_cache(q, k, v, wq, wk, inv_freq, positions, slots, k_cache
     return q_out
 
 
+@functools.lru_cache(maxsize=None)
 def attn_decode_workspace_size(Hq, Hk, d, dtype) -> int:
     n = load().delta_rule_attn_decode_workspace_size(Hq, Hk, d, dtype)
     if n == ctypes.c_size_t(-1).value:
@@ -805,7 +832,7 @@ def delta_rule_attn_decode(q, k_cache, v_cache, table, lens, scale=None, window=
     if table.shape[0] != R:
         raise ValueError(f"table: expected {R} rows, got {table.shape[0]}")
     if out is None:
-        out = torch.empty((R, Hq, d), dtype=dt, device=dev)
+        out = _dense_like(q)
     lse = torch.empty((R, Hq), dtype=torch.float32, device=dev) if want_lse else None
     need = attn_decode_workspace_size(Hq, Hk, d, DTYPES[dt])
     if workspace is None or workspace.numel() < need:

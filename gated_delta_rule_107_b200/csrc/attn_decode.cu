@@ -9,12 +9,14 @@
 // What bounds it is reading the cache once: a key head's rows serve the G = Hq / Hk heads of its
 // group, 2 G flops a byte in bf16, far below what the tensor cores need to be busy; so the design
 // is about bytes in flight and an even split.
-//   Work.  The unit is a tile of 16 tokens of one (request, key head[, block of its query heads]).
+//   Work.  The piece is a tile of 16 tokens of one (request, key head[, block of its query heads]).
 //     The tiles of all requests form one list, cut into equal contiguous runs, one per CTA, however
-//     ragged the lengths: a run may hold parts of several (request, head) segments.  A segment
-//     inside one CTA's run is finished there; one that crosses runs leaves fp32 partials (m, l, o)
-//     in the workspace, at most two a CTA, which k_attn_join adds in the order of the runs (no
-//     atomics: results do not change from run to run).
+//     ragged the lengths: a run may hold parts of several (request, head) segments.  A segment's
+//     start and join cost a CTA about as long as COST tiles, so each counts that much more in the
+//     list (units; the tiles come behind them).  A segment inside one CTA's run is finished there;
+//     one that crosses runs leaves fp32 partials (m, l, o) in the workspace, at most two a CTA,
+//     which k_attn_join adds in the order of the runs (no atomics: results do not change from run
+//     to run).
 //   Loads.  Each warp takes every fourth tile of its CTA's run through a pipeline of its own in
 //     shared memory, 16-byte asynchronous copies, rows swizzled by 16-byte chunk; the pipeline
 //     runs on across segments, and warps meet only at a segment's end.
@@ -33,6 +35,7 @@
 #include <math_constants.h>
 
 #include "attn_decode.cuh"
+#include "prepost.cuh"
 
 namespace dr {
 namespace ad {
@@ -40,13 +43,18 @@ namespace ad {
 constexpr int WARPS = 4, THREADS = WARPS * 32;
 constexpr int TILE = 16;          // tokens a warp takes at a time
 constexpr int MAX_CTAS = 296;     // two a SM (one where registers or shared memory hold no second)
-constexpr int MIN_TILES = WARPS;  // a CTA's run is at least one tile a warp
+constexpr int MIN_UNITS = WARPS;  // a CTA's run is at least one tile a warp
+#ifndef PROBE_COST
+#define PROBE_COST 4
+#endif
+constexpr int COST = PROBE_COST;           // of a segment, in tiles
 constexpr float LOG2E = 1.44269504088896340736f, LN2 = 0.69314718055994530942f;
 
 struct Args {
     AttnDecode a;
     int G, GB, RB;       // query heads of a group; heads of a block; blocks of a group
-    float *part;         // [2 * MAX_CTAS][GB][D + 2]: o (not divided by l), m, l
+    float *part;         // [2 * MAX_CTAS][GB][D]: o, not divided by l
+    float2 *ml;          // [2 * MAX_CTAS][GB]: m, l
     int4 *head;          // [MAX_CTAS]: the split segment that begins in a CTA: request, key head, block, last CTA
     float scale2;
     FastDiv by_page;
@@ -88,8 +96,8 @@ __device__ __forceinline__ uint32_t pack(float lo, float hi) {
     return *reinterpret_cast<const uint32_t *>(&x);
 }
 
-// a partial sum l at maximum m, at the joint maximum mx (l = 0: nothing seen, m = -inf; a NaN stays)
-__device__ __forceinline__ float part_of(float l, float m, float mx) { return l == 0.f ? 0.f : l * ex2(m - mx); }
+// log of the sum l (base 2 maximum m); nothing seen: -inf; a NaN stays
+__device__ __forceinline__ float lse_of(float m, float l) { return l > 0.f ? (m + log2f(l)) * LN2 : (l == l ? -CUDART_INF_F : l); }
 
 // The visible tokens of request r and its tiles.
 struct Span {
@@ -104,17 +112,19 @@ struct Span {
     }
 };
 
-// A place in the list of tiles: request r, segment (key head, block of query heads) of it, tile.
+// A place in the list: request r, segment (key head, block of query heads) of it, tile; `unit` is the
+// tile's place in the list from the beginning of the CTA's run.
 struct Place {
-    int r, seg, tile;
+    int r, seg, tile, unit;
     Span sp;
 };
+__device__ __forceinline__ long long units_of(const Span &sp) { return sp.tiles > 0 ? sp.tiles + COST : 0; }
 
-// What the CTA does: its run [a0, a1) of the list, the place of a0, and where a0's segment began.
+// The CTA's run [u0, u0 + len) of the list's units, `per` units for every run but the last; the
+// request r0 in which it begins, whose first unit is `base`.
 struct Run {
-    long long a0, a1, per;
-    int r0;
-    long long base;  // the list's index of request r0's first tile
+    long long u0, base;
+    int len, per, r0;
 };
 
 // All threads of the CTA; every CTA finds its run from the lengths alone.
@@ -127,7 +137,7 @@ __device__ __forceinline__ Run find_run(const Args &x, int segs) {
     Span sp;
     for (int r = b0; r < b1; ++r) {
         sp.set(a, r);
-        mine += (long long)sp.tiles * segs;
+        mine += units_of(sp) * segs;
     }
     long long inc = mine;
 #pragma unroll
@@ -143,47 +153,51 @@ __device__ __forceinline__ Run find_run(const Args &x, int segs) {
         total += wsum[w];
     }
     Run run;
-    run.per = max((long long)MIN_TILES, (total + gridDim.x - 1) / gridDim.x);
-    run.a0 = min(total, run.per * blockIdx.x);
-    run.a1 = min(total, run.a0 + run.per);
-    if (run.a0 < run.a1 && before <= run.a0 && run.a0 < before + mine) {
+    run.per = (int)max((long long)MIN_UNITS, (total + gridDim.x - 1) / gridDim.x);
+    run.u0 = min(total, (long long)run.per * blockIdx.x);
+    run.len = (int)min(total - run.u0, (long long)run.per);
+    if (run.len > 0 && before <= run.u0 && run.u0 < before + mine) {
         int r = b0;
         for (; r < b1; ++r) {
             sp.set(a, r);
-            const long long w = (long long)sp.tiles * segs;
-            if (run.a0 < before + w) break;
+            const long long w = units_of(sp) * segs;
+            if (run.u0 < before + w) break;
             before += w;
         }
         found[0] = r;
         found[1] = before;
     }
     __syncthreads();
-    run.r0 = run.a0 < run.a1 ? (int)found[0] : 0;
-    run.base = run.a0 < run.a1 ? found[1] : 0;
+    run.r0 = run.len > 0 ? (int)found[0] : 0;
+    run.base = run.len > 0 ? found[1] : 0;
     return run;
 }
 
-__device__ __forceinline__ void skip_empty(Place &pl, const AttnDecode &a) {
-    while (pl.sp.tiles == 0 && pl.r + 1 < a.R) pl.sp.set(a, ++pl.r);
-}
-// moves `by` tiles on; only called while the place stays inside the list
+constexpr int NOWHERE = 0x7fffffff;  // the unit of a place behind the list
+
+// moves `by` tiles on
 __device__ __forceinline__ void advance(Place &pl, int by, int segs, const AttnDecode &a) {
     pl.tile += by;
+    pl.unit += by;
     while (pl.tile >= pl.sp.tiles) {
         pl.tile -= pl.sp.tiles;
+        pl.unit += COST;
         if (++pl.seg == segs) {
             pl.seg = 0;
-            if (pl.r + 1 >= a.R) return;
-            pl.sp.set(a, ++pl.r);
-            skip_empty(pl, a);
-            if (pl.sp.tiles == 0) return;
+            do {
+                if (++pl.r >= a.R) {
+                    pl.unit = NOWHERE;
+                    return;
+                }
+                pl.sp.set(a, pl.r);
+            } while (pl.sp.tiles == 0);
         }
     }
 }
 
 // One warp's pipeline of tiles.  A stage is the K rows, then the V rows, of 16 tokens.
 template <typename E, int D, int STAGES> struct Pipe {
-    static constexpr int ROW = D * (int)sizeof(E), CPR = ROW / 16;  // bytes, 16-byte chunks of a row
+    static constexpr int ROW = D * (int)sizeof(E), CPR = ROW / 16, E16 = 16 / (int)sizeof(E);  // bytes, 16-byte chunks of a row
     static constexpr int HALF = TILE * ROW, STAGE = 2 * HALF;
     static constexpr int RPI = 32 / (CPR < 32 ? CPR : 32);          // rows a warp copies with one instruction
     static_assert(CPR <= 32, "a row is at most one instruction");
@@ -219,7 +233,7 @@ template <typename E, int D, int STAGES> struct Pipe {
         const int lane = threadIdx.x & 31;
         const bool seen = w.pg >= 0 && w.pg < a.n_pages;
         const uint32_t live = __ballot_sync(0xffffffffu, seen) & 0xffffu;
-        const int c = lane % CPR, row0 = lane / CPR, e16 = 16 / (int)sizeof(E);
+        const int c = lane % CPR, row0 = lane / CPR, e16 = E16;
         const size_t inside = ((size_t)w.in * a.Hk + w.h) * D;
         const size_t ko = seen ? (size_t)w.pg * a.kps + inside : 0, vo = seen ? (size_t)w.pg * a.vps + inside : 0;
         if (x.whole && live == 0xffffu) {  // 16 rows of one page: evenly spaced from the first one's
@@ -247,17 +261,22 @@ template <typename E, int D, int STAGES> struct Pipe {
 
 // ------------------------------------------------------------------ one warp's arithmetic
 // Each keeps, for the heads of a block, m (base 2), l and o, and offers
-//   start(q row of the block's first head, heads), tile(stage, live), finish(): l summed over lanes,
-//   each(f): f(head, channel, o) for every value the lane holds, and m / l of a head by stat().
+//   fetch(q row of the block's first head, heads): reads the queries; begin(): they are the ones from now
+//   tile(stage, live)
+//   finish(m, l, o): l summed over lanes, all three to shared memory, o as [head][slot_of(head, channel)]
+
+// where a head's channel lies in a row of o in shared memory: blocks of 8 channels exchanged so that
+// the matrix fragments (8 channels of four pairs of heads at once) fall into different banks
+__device__ __forceinline__ int slot_of(int head, int ch) { return ch ^ ((head >> 1 & 3) << 3); }
 
 template <int D, int NT> struct Mma {  // bf16: blocks of 8 NT heads
     typedef __nv_bfloat16 E;
     static constexpr int GB = 8 * NT, STAGES = (D == 128 ? 3 : 6), CTAS = MAX_CTAS;
     typedef Pipe<E, D, STAGES> P;
-    uint32_t q[D / 16][NT][2];
+    uint32_t q[D / 16][NT][2], qn[D / 16][NT][2];
     float o[D / 16][NT][4], m[NT][2], l[NT][2];
 
-    __device__ __forceinline__ void start(const E *src, int heads) {
+    __device__ __forceinline__ void fetch(const E *src, int heads) {
         const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
 #pragma unroll
         for (int k = 0; k < D / 16; ++k)
@@ -265,18 +284,21 @@ template <int D, int NT> struct Mma {  // bf16: blocks of 8 NT heads
             for (int j = 0; j < NT; ++j) {
                 const bool in = j * 8 + g < heads;
                 const E *s = src + (in ? j * 8 + g : 0) * D + k * 16 + 2 * t;
-                q[k][j][0] = in ? *reinterpret_cast<const uint32_t *>(s) : 0u;
-                q[k][j][1] = in ? *reinterpret_cast<const uint32_t *>(s + 8) : 0u;
+                qn[k][j][0] = in ? *reinterpret_cast<const uint32_t *>(s) : 0u;
+                qn[k][j][1] = in ? *reinterpret_cast<const uint32_t *>(s + 8) : 0u;
             }
-        clear();
     }
-    __device__ __forceinline__ void clear() {
+    __device__ __forceinline__ void begin() {
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
             m[j][0] = m[j][1] = -CUDART_INF_F;
             l[j][0] = l[j][1] = 0.f;
 #pragma unroll
-            for (int k = 0; k < D / 16; ++k) o[k][j][0] = o[k][j][1] = o[k][j][2] = o[k][j][3] = 0.f;
+            for (int k = 0; k < D / 16; ++k) {
+                q[k][j][0] = qn[k][j][0];
+                q[k][j][1] = qn[k][j][1];
+                o[k][j][0] = o[k][j][1] = o[k][j][2] = o[k][j][3] = 0.f;
+            }
         }
     }
     __device__ __forceinline__ void tile(uint32_t stage, uint32_t live, float scale2, void *) {
@@ -369,29 +391,25 @@ template <int D, int NT> struct Mma {  // bf16: blocks of 8 NT heads
             }
         }
     }
-    __device__ __forceinline__ void finish() {
-#pragma unroll
-        for (int d = 4; d < 32; d <<= 1)
-#pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                l[j][0] += __shfl_xor_sync(0xffffffffu, l[j][0], d);
-                l[j][1] += __shfl_xor_sync(0xffffffffu, l[j][1], d);
-            }
-    }
-    // the heads of which the lane holds values: 2 NT
-    static constexpr int HEADS = 2 * NT, VALS = HEADS * (D / 8);
-    static __device__ __forceinline__ int head_of(int i) { return (i >> 1) * 8 + 2 * (threadIdx.x & 3) + (i & 1); }
-    __device__ __forceinline__ float &mm(int i) { return m[i >> 1][i & 1]; }
-    __device__ __forceinline__ float &ll(int i) { return l[i >> 1][i & 1]; }
-    template <typename F> __device__ __forceinline__ void each(F f) {
-        const int g = (threadIdx.x & 31) >> 2;
+    __device__ __forceinline__ void finish(float *sm, float *sl, float *so) {
+        const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
 #pragma unroll
         for (int j = 0; j < NT; ++j)
 #pragma unroll
-            for (int k = 0; k < D / 16; ++k)
+            for (int i = 0; i < 2; ++i) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    f(2 * j + (i & 1), head_of(2 * j + (i & 1)), k * 16 + g + (i >> 1) * 8, o[k][j][i]);
+                for (int d = 4; d < 32; d <<= 1) l[j][i] += __shfl_xor_sync(0xffffffffu, l[j][i], d);
+                const int head = j * 8 + 2 * t + i;
+                if (g == 0) {
+                    sm[head] = m[j][i];
+                    sl[head] = l[j][i];
+                }
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) {
+                    so[head * D + slot_of(head, k * 16 + g)] = o[k][j][i];
+                    so[head * D + slot_of(head, k * 16 + g + 8)] = o[k][j][i + 2];
+                }
+            }
     }
     static constexpr int EXTRA = 0;  // bytes of shared memory of the warp's own
 };
@@ -403,15 +421,18 @@ template <int D, int H> struct Simt {  // fp32: blocks of H heads, at most 8
     float o[GB][NC], m[GB], l[GB];
     static constexpr int EXTRA = (GB * D + TILE * GB) * 4;  // the block's queries, the tile's p
 
-    float *qs, *ps;
-    __device__ __forceinline__ void start(const E *src, int heads) {
+    float *qs, *ps, qn[GB * D / 32];
+    __device__ __forceinline__ void fetch(const E *src, int heads) {
+        const int lane = threadIdx.x & 31;
+#pragma unroll
+        for (int i = 0; i < GB * D / 32; ++i) qn[i] = (i * 32 + lane) / D < heads ? src[i * 32 + lane] : 0.f;
+    }
+    __device__ __forceinline__ void begin() {
         const int lane = threadIdx.x & 31;
         __syncwarp();
-        for (int i = lane; i < GB * D; i += 32) qs[i] = i / D < heads ? src[i] : 0.f;
+#pragma unroll
+        for (int i = 0; i < GB * D / 32; ++i) qs[i * 32 + lane] = qn[i];
         __syncwarp();
-        clear();
-    }
-    __device__ __forceinline__ void clear() {
 #pragma unroll
         for (int h = 0; h < GB; ++h) {
             m[h] = -CUDART_INF_F;
@@ -473,20 +494,18 @@ template <int D, int H> struct Simt {  // fp32: blocks of H heads, at most 8
         }
         __syncwarp();  // ps is free for the next tile
     }
-    __device__ __forceinline__ void finish() {
-#pragma unroll
-        for (int h = 0; h < GB; ++h) l[h] = warp_sum(l[h]);
-    }
-    static constexpr int HEADS = GB, VALS = GB * NC;
-    static __device__ __forceinline__ int head_of(int i) { return i; }
-    __device__ __forceinline__ float &mm(int i) { return m[i]; }
-    __device__ __forceinline__ float &ll(int i) { return l[i]; }
-    template <typename F> __device__ __forceinline__ void each(F f) {
+    __device__ __forceinline__ void finish(float *sm, float *sl, float *so) {
         const int lane = threadIdx.x & 31;
 #pragma unroll
-        for (int h = 0; h < GB; ++h)
+        for (int h = 0; h < GB; ++h) {
+            l[h] = warp_sum(l[h]);
+            if (lane == 0) {
+                sm[h] = m[h];
+                sl[h] = l[h];
+            }
 #pragma unroll
-            for (int c = 0; c < NC; ++c) f(h, h, lane * NC + c, o[h][c]);
+            for (int c = 0; c < NC; ++c) so[h * D + slot_of(h, lane * NC + c)] = o[h][c];
+        }
     }
 };
 
@@ -499,17 +518,14 @@ template <class C, int D> __global__ void __launch_bounds__(THREADS) k_attn(cons
     constexpr int GB = C::GB, STAGES = C::STAGES;
     extern __shared__ __align__(128) char smem[];
     __shared__ float sm_m[WARPS][GB], sm_l[WARPS][GB];
-    __shared__ float sm_o[GB][D + 1];
+    __shared__ int sm_at[WARPS];
+    static_assert(GB * D * 4 <= P::STAGE, "a warp's o fits a stage");
     const AttnDecode &a = x.a;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int segs = a.Hk * x.RB;
     asm volatile("griddepcontrol.launch_dependents;");  // the join may take its places; it waits for this kernel's end
     const Run run = find_run(x, segs);
-    if (run.a0 >= run.a1) {
-        if (tid == 0) x.head[blockIdx.x] = make_int4(-1, 0, 0, 0);
-        // requests that see nothing, shared out over the CTAs below
-    }
-    for (int r = blockIdx.x; r < a.R; r += gridDim.x) {
+    for (int r = blockIdx.x; r < a.R; r += gridDim.x) {  // requests that see nothing
         Span sp;
         sp.set(a, r);
         if (sp.tiles > 0) continue;
@@ -517,143 +533,126 @@ template <class C, int D> __global__ void __launch_bounds__(THREADS) k_attn(cons
         if (a.lse)
             for (int i = tid; i < a.Hq; i += THREADS) a.lse[(size_t)r * a.Hq + i] = -CUDART_INF_F;
     }
-    if (run.a0 >= run.a1) return;
+    // the place of the run's first tile
+    Place here;
+    here.unit = NOWHERE;
+    if (run.len > 0) {
+        here.r = run.r0;
+        here.sp.set(a, here.r);
+        const long long in = run.u0 - run.base;  // not negative, inside request r0
+        here.seg = (int)(in / units_of(here.sp));
+        const int off = (int)(in - here.seg * units_of(here.sp)) - COST;
+        here.tile = max(off, 0);
+        here.unit = max(-off, 0);
+    }
+    if (here.unit >= run.len) {  // no tile in the run
+        if (tid == 0) x.head[blockIdx.x] = make_int4(-1, 0, 0, 0);
+        return;
+    }
 
     char *mine = smem + warp * warp_bytes<C, D>();
     const uint32_t stages = smem_u32(mine);
-    // the place of the run's first tile
-    Place here;
-    here.r = run.r0;
-    here.sp.set(a, here.r);
-    long long in = run.a0 - run.base;
-    here.seg = (int)(in / here.sp.tiles);
-    here.tile = (int)(in - (long long)here.seg * here.sp.tiles);
-
-    // the warp's loads run STAGES - 1 tiles ahead of its arithmetic, the table's entries one more
-    const int count = (int)(run.a1 - run.a0);  // tiles of the CTA; warp w takes w, w + WARPS, ...
+    // the warp's loads run STAGES - 1 tiles ahead of its arithmetic, the table's entries one more;
+    // warp w takes the run's tiles w, w + WARPS, ...
     __shared__ uint32_t lives[WARPS][STAGES];
     Place next = here;
     typename P::Want ahead[STAGES] = {};
-    int known = warp;  // the tile that `next` is at
-    if (known < count) {
-        advance(next, warp, segs, a);
-        ahead[0] = P::want(x, next);
-    }
+    bool there[STAGES];
 #pragma unroll
-    for (int i = 1; i < STAGES; ++i) {
-        known += WARPS;
-        if (known < count) {
-            advance(next, WARPS, segs, a);
-            ahead[i] = P::want(x, next);
-        }
+    for (int i = 0; i < STAGES; ++i) {
+        if (next.unit < run.len) advance(next, i == 0 ? warp : WARPS, segs, a);
+        there[i] = next.unit < run.len;
+        if (there[i]) ahead[i] = P::want(x, next);
     }
-    int put = 0, got = 0, issued = warp;
-    auto issue = [&](const typename P::Want &w) {
-        if (issued < count) {
+    int put = 0, got = 0;
+    auto issue = [&](const typename P::Want &w, bool is) {
+        if (is) {
             const uint32_t bits = P::load(stages + put * P::STAGE, x, w);
             if (lane == 0) lives[warp][put] = bits;
         }
-        issued += WARPS;
         cp_commit();
         put = put + 1 == STAGES ? 0 : put + 1;
     };
 #pragma unroll
-    for (int i = 0; i < STAGES - 1; ++i) issue(ahead[i]);
+    for (int i = 0; i < STAGES - 1; ++i) issue(ahead[i], there[i]);
     typename P::Want coming = ahead[STAGES - 1];
+    bool comes = there[STAGES - 1];
 
     C c;
     if constexpr (C::EXTRA > 0) {
         c.qs = reinterpret_cast<float *>(mine + STAGES * P::STAGE);
         c.ps = c.qs + GB * D;
     }
-    int done = 0;  // tiles of the CTA's run before the current segment
-    int mytile = warp;
-    for (int part = 0; done < count; ++part) {
+    int done = 0, mytile = warp;  // the run's tiles before the current segment; the warp's next one
+    auto fetch = [&](const Place &pl) {
+        const int h = pl.seg / x.RB, rb = pl.seg - h * x.RB;
+        c.fetch((const E *)a.q + ((size_t)pl.r * a.Hq + h * x.G + rb * GB) * D, min(GB, x.G - rb * GB));
+    };
+    fetch(here);
+    for (int part = 0; here.unit < run.len; ++part) {
         const int h = here.seg / x.RB, rb = here.seg - h * x.RB, head0 = h * x.G + rb * GB;
         const int heads = min(GB, x.G - rb * GB);
-        const int upto = min(count, done + here.sp.tiles - here.tile);  // the segment's tiles in this run end here
-        c.start((const E *)a.q + ((size_t)here.r * a.Hq + head0) * D, heads);
+        const int rest = here.sp.tiles - here.tile, now = min(rest, run.len - here.unit), upto = done + now;
+        const bool whole = here.tile == 0 && now == rest;
+        c.begin();
         for (; mytile < upto; mytile += WARPS) {
             cp_wait<STAGES - 2>();
             __syncwarp();
             const uint32_t bits = lives[warp][got];
-            issue(coming);
-            known += WARPS;
-            if (known < count) {
-                advance(next, WARPS, segs, a);
-                coming = P::want(x, next);
-            }
+            issue(coming, comes);
+            if (comes) advance(next, WARPS, segs, a);
+            comes = next.unit < run.len;
+            if (comes) coming = P::want(x, next);
             c.tile(stages + got * P::STAGE, bits, x.scale2, mine + got * P::STAGE);
             got = got + 1 == STAGES ? 0 : got + 1;
             __syncwarp();
         }
-        c.finish();
-        // join the warps
-        __syncthreads();  // the join of the segment before is read
-#pragma unroll
-        for (int i = 0; i < C::HEADS; ++i) {
-            sm_m[warp][C::head_of(i)] = c.mm(i);
-            sm_l[warp][C::head_of(i)] = c.ll(i);
-        }
+        // the queries of the segment behind this one, while the warps join
+        Place then = here;
+        advance(then, rest, segs, a);
+        if (then.unit < run.len) fetch(then);
+        // each warp's o goes to the stage that it will fill next, and which holds nothing now
+        c.finish(sm_m[warp], sm_l[warp], reinterpret_cast<float *>(mine + put * P::STAGE));
+        if (lane == 0) sm_at[warp] = warp * warp_bytes<C, D>() + put * P::STAGE;
         __syncthreads();
-        float f[C::HEADS], mj[C::HEADS], lj[C::HEADS];
-#pragma unroll
-        for (int i = 0; i < C::HEADS; ++i) {
-            const int hd = C::head_of(i);
-            float mx = sm_m[0][hd];
+        const size_t slot = 2 * blockIdx.x + (part > 0);
+        for (int i = tid; i < heads * (D / 8); i += THREADS) {
+            const int hd = i / (D / 8), ch = (i - hd * (D / 8)) * 8;
+            float mx = sm_m[0][hd], s = 0.f, o[8] = {};
 #pragma unroll
             for (int w = 1; w < WARPS; ++w) mx = fmaxf(mx, sm_m[w][hd]);
-            float s = 0.f;
 #pragma unroll
-            for (int w = 0; w < WARPS; ++w) s += part_of(sm_l[w][hd], sm_m[w][hd], mx);
-            f[i] = c.ll(i) == 0.f ? 0.f : ex2(c.mm(i) - mx);
-            mj[i] = mx;
-            lj[i] = s;
-        }
-        for (int w = 0; w < WARPS; ++w) {
-            if (warp == w)
-                c.each([&](int i, int hd, int ch, float o) {
-                    const float y = o * f[i];
-                    sm_o[hd][ch] = w == 0 ? y : sm_o[hd][ch] + y;
-                });
-            __syncthreads();
-        }
-        const bool begins = here.tile == 0, ends = done + here.sp.tiles - here.tile <= count;
-        if (begins && ends) {
-            E *dst = (E *)a.out + ((size_t)here.r * a.Hq + head0) * D;
-            for (int i = tid; i < heads * D; i += THREADS) {
-                const int hd = i / D;
-                float mx = sm_m[0][hd], s = 0.f;
-                for (int w = 1; w < WARPS; ++w) mx = fmaxf(mx, sm_m[w][hd]);
-                for (int w = 0; w < WARPS; ++w) s += part_of(sm_l[w][hd], sm_m[w][hd], mx);
-                dst[i] = from_f<E>(s > 0.f ? sm_o[hd][i - hd * D] / s : (s == s ? 0.f : s));
-                if (a.lse && i % D == 0)
-                    a.lse[(size_t)here.r * a.Hq + head0 + hd] = s > 0.f ? (mx + log2f(s)) * LN2 : (s == s ? -CUDART_INF_F : s);
+            for (int w = 0; w < WARPS; ++w) {
+                const float l = sm_l[w][hd], f = l == 0.f ? 0.f : ex2(sm_m[w][hd] - mx);  // l = 0: m may be -inf
+                s += l * f;
+                const float4 *p = reinterpret_cast<const float4 *>(smem + sm_at[w]) + (hd * D + slot_of(hd, ch)) / 4;
+                const float4 u = p[0], v = p[1];
+                o[0] += u.x * f; o[1] += u.y * f; o[2] += u.z * f; o[3] += u.w * f;
+                o[4] += v.x * f; o[5] += v.y * f; o[6] += v.z * f; o[7] += v.w * f;
             }
-        } else {
-            float *dst = x.part + (size_t)(2 * blockIdx.x + (part > 0)) * GB * (D + 2);
-            for (int i = tid; i < GB * D; i += THREADS) dst[i / D * (D + 2) + i % D] = sm_o[i / D][i % D];
-            if (warp == 0)
+            if (whole) {
+                const float inv = s > 0.f ? 1.f / s : (s == s ? 0.f : s);
 #pragma unroll
-                for (int i = 0; i < C::HEADS; ++i) {
-                    dst[C::head_of(i) * (D + 2) + D] = mj[i];
-                    dst[C::head_of(i) * (D + 2) + D + 1] = lj[i];
-                }
+                for (int k = 0; k < 8; ++k) o[k] *= inv;
+                E *dst = (E *)a.out + ((size_t)here.r * a.Hq + head0 + hd) * D + ch;
+#pragma unroll
+                for (int k = 0; k < 8; k += P::E16) pp::Vec<E, P::E16>::st(dst + k, o + k);
+                if (a.lse && ch == 0) a.lse[(size_t)here.r * a.Hq + head0 + hd] = lse_of(mx, s);
+            } else {
+                float4 *dst = reinterpret_cast<float4 *>(x.part + (slot * GB + hd) * D + ch);
+                dst[0] = make_float4(o[0], o[1], o[2], o[3]);
+                dst[1] = make_float4(o[4], o[5], o[6], o[7]);
+                if (ch == 0) x.ml[slot * GB + hd] = make_float2(mx, s);
+            }
         }
-        const int here_left = done + here.sp.tiles - here.tile;
-        if (tid == 0 && here_left >= count) {  // the run's last segment
+        if (tid == 0 && then.unit >= run.len) {  // the run's last segment
             int last = -1;
-            if (begins && !ends) {
-                const long long end = run.a0 + done + here.sp.tiles;  // the list's index behind the segment
-                last = (int)((end - 1) / run.per);
-            }
+            if (here.tile == 0 && !whole) last = (int)((run.u0 + here.unit + rest - 1) / run.per);  // its last tile's run
             x.head[blockIdx.x] = last < 0 ? make_int4(-1, 0, 0, 0) : make_int4(here.r, h, rb | (part > 0) << 16, last);
         }
+        __syncthreads();  // the stages and the statistics are read
         done = upto;
-        if (done < count) {
-            here.tile = here.sp.tiles - 1;
-            advance(here, 1, segs, a);
-        }
+        here = then;
     }
 }
 
@@ -668,10 +667,10 @@ template <typename E, int D> __global__ void __launch_bounds__(256) k_attn_join(
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n = hd.w - (int)blockIdx.x + 1;
     constexpr int NC = D / 32;
     auto part = [&](int i) {  // part i: the CTA's second slot only for a segment that begins behind another
-        return x.part + ((size_t)(2 * (blockIdx.x + i) + (i == 0 ? slot0 : 0)) * GB + in) * (D + 2);
+        return (size_t)(2 * (blockIdx.x + i) + (i == 0 ? slot0 : 0)) * GB + in;
     };
     float m = -CUDART_INF_F;
-    for (int i = threadIdx.x; i < n; i += 256) m = fmaxf(m, part(i)[D]);
+    for (int i = threadIdx.x; i < n; i += 256) m = fmaxf(m, x.ml[part(i)].x);
     m = warp_max(m);
     if (lane == 0) wm[warp] = m;
     __syncthreads();
@@ -679,9 +678,11 @@ template <typename E, int D> __global__ void __launch_bounds__(256) k_attn_join(
     float o[NC] = {}, l = 0.f;
 #pragma unroll 4
     for (int i = warp; i < n; i += 8) {
-        const float *p = part(i);
-        const float f = p[D + 1] == 0.f ? 0.f : ex2(p[D] - m);
-        l += p[D + 1] * f;
+        const size_t at = part(i);
+        const float2 ml = x.ml[at];
+        const float *p = x.part + at * D;
+        const float f = ml.y == 0.f ? 0.f : ex2(ml.x - m);
+        l += ml.y * f;
 #pragma unroll
         for (int c = 0; c < NC; ++c) o[c] += f * p[c * 32 + lane];
     }
@@ -697,7 +698,7 @@ template <typename E, int D> __global__ void __launch_bounds__(256) k_attn_join(
         for (int w = 0; w < 8; ++w) s += red[w][c];
         ((E *)x.a.out)[row * D + c] = from_f<E>(l > 0.f ? s / l : (l == l ? 0.f : l));
     }
-    if (threadIdx.x == 0 && x.a.lse) x.a.lse[row] = l > 0.f ? (m + log2f(l)) * LN2 : (l == l ? -CUDART_INF_F : l);
+    if (threadIdx.x == 0 && x.a.lse) x.a.lse[row] = lse_of(m, l);
 }
 
 template <class C, int D> static cudaError_t launch(Args x, cudaStream_t s) {
@@ -705,13 +706,14 @@ template <class C, int D> static cudaError_t launch(Args x, cudaStream_t s) {
     x.GB = C::GB;
     x.RB = (x.G + C::GB - 1) / C::GB;
     x.head = (int4 *)a.ws;
-    x.part = (float *)((char *)a.ws + MAX_CTAS * sizeof(int4));
+    x.ml = (float2 *)(x.head + MAX_CTAS);
+    x.part = (float *)(x.ml + 2 * MAX_CTAS * C::GB);  // 16-byte aligned
     const int smem = smem_bytes<C, D>();
     cudaError_t e = cudaFuncSetAttribute(k_attn<C, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     // no more CTAs than the tables have room for runs
-    const double tiles = (double)a.R * a.Hk * x.RB * ((double)a.width * a.page / TILE + 1);
-    const int ctas = tiles / MIN_TILES < C::CTAS - 1 ? (int)(tiles / MIN_TILES) + 1 : C::CTAS;
+    const double tiles = (double)a.R * a.Hk * x.RB * ((double)a.width * a.page / TILE + 1 + COST);
+    const int ctas = tiles / MIN_UNITS < C::CTAS - 1 ? (int)(tiles / MIN_UNITS) + 1 : C::CTAS;
     k_attn<C, D><<<ctas, THREADS, smem, s>>>(x);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
