@@ -10,7 +10,7 @@
 //
 // A token's angles are the same for all its heads, so a group of d / (2 VEC) lanes takes one token
 // and walks its heads: each lane owns two 16-byte vectors of every row, chosen so that the two
-// halves of each channel pair meet in one lane, and computes its own angles once per token.  The
+// channels of each pair meet in one lane, and computes its own angles once per token.  The
 // angle is reduced to a fraction of a turn in 64 bits (position * inv_freq / 2 pi, minus the
 // nearest whole number), because in 32 bits a position of 10^6 leaves an error of 0.06 rad; the
 // fraction is then exact enough in 32 bits.
@@ -28,20 +28,116 @@ constexpr int PF_FWD = 5, PF_BWD = 5;  // slots of the rows ahead
 constexpr int FWD_CTAS = 148 * 64, BWD_CTAS = 1184;  // at most; the backward's are also its partial sums
 constexpr double INV_2PI = 0.15915494309189533577;
 
-using pp::Vec;
+// Two fp32 numbers in a 64-bit register pair: Blackwell's packed arithmetic takes one issue slot
+// for both, and these kernels are bound by issue slots once their loads are far enough ahead.
+typedef unsigned long long f2;
+__device__ __forceinline__ f2 mk(float lo, float hi) {
+    f2 d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+    return d;
+}
+__device__ __forceinline__ void un(f2 x, float &lo, float &hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(x)); }
+__device__ __forceinline__ f2 mul(f2 a, f2 b) {
+    f2 d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ f2 fma(f2 a, f2 b, f2 c) {
+    f2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ float sum2(f2 x) {
+    float a, b;
+    un(x, a, b);
+    return a + b;
+}
 
-// The lanes of a token and the two vectors a lane owns of each row (indexes of 16-byte vectors).
-template <typename E, int D> struct Lay {
-    static constexpr int VEC = 16 / (int)sizeof(E), LPT = D / (2 * VEC), TPW = 32 / LPT;
-    int ia, ib;
-    bool turned;  // the two vectors take part in the rotation
-    __device__ __forceinline__ Lay(int j, int rot) {
+// The lanes of a token and what a lane holds of each row: two 16-byte vectors (indexes ia, ib),
+// chosen so that the two channels of each pair meet in the lane, as VEC first and VEC second
+// channels of pairs, two to a register pair: channels i of the vectors a and b (pairs (i, i + rot/2)),
+// or the even and the odd channels of both (interleaved).  Channels behind rot are held alike and
+// turned by nothing.
+template <typename E, int D, bool INTER> struct Lay {
+    static constexpr int VEC = 16 / (int)sizeof(E), N2 = VEC / 2, LPT = D / (2 * VEC), TPW = 32 / LPT;
+    int j, ia, ib;
+    bool turned;  // the lane's pairs take part in the rotation
+    __device__ __forceinline__ Lay(int j_, int rot) : j(j_) {
         const int half = rot / (2 * VEC);
         turned = j < half;
         ia = turned ? j : 2 * j;
         ib = turned ? j + half : 2 * j + 1;
     }
+    // the channel of the i-th first (0) or second (1) number
+    __device__ __forceinline__ int channel(int second, int i) const {
+        if (INTER) return (i < VEC / 2 ? ia : ib) * VEC + 2 * (i % (VEC / 2)) + second;
+        return (second ? ib : ia) * VEC + i;
+    }
+    // the pair (its index into inv_freq) of the i-th numbers
+    __device__ __forceinline__ int pair(int i) const {
+        return INTER ? (i < VEC / 2 ? ia : ib) * (VEC / 2) + i % (VEC / 2) : j * VEC + i;
+    }
 };
+
+__device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
+// a row's two vectors to numbers and back
+template <bool INTER> __device__ __forceinline__ void open(const uint4 &a, const uint4 &b, f2 *A, f2 *B, __nv_bfloat16 *) {
+    const uint32_t u[4] = {a.x, a.y, a.z, a.w}, v[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (INTER) {
+            const uint32_t p = i < 2 ? u[2 * i] : v[2 * i - 4], q = i < 2 ? u[2 * i + 1] : v[2 * i - 3];
+            A[i] = mk(lo_f(p), lo_f(q));
+            B[i] = mk(hi_f(p), hi_f(q));
+        } else {
+            A[i] = mk(lo_f(u[i]), hi_f(u[i]));
+            B[i] = mk(lo_f(v[i]), hi_f(v[i]));
+        }
+    }
+}
+template <bool INTER> __device__ __forceinline__ void open(const uint4 &a, const uint4 &b, f2 *A, f2 *B, float *) {
+    const float u[4] = {__uint_as_float(a.x), __uint_as_float(a.y), __uint_as_float(a.z), __uint_as_float(a.w)};
+    const float v[4] = {__uint_as_float(b.x), __uint_as_float(b.y), __uint_as_float(b.z), __uint_as_float(b.w)};
+    if (INTER) {
+        A[0] = mk(u[0], u[2]); B[0] = mk(u[1], u[3]);
+        A[1] = mk(v[0], v[2]); B[1] = mk(v[1], v[3]);
+    } else {
+        A[0] = mk(u[0], u[1]); A[1] = mk(u[2], u[3]);
+        B[0] = mk(v[0], v[1]); B[1] = mk(v[2], v[3]);
+    }
+}
+__device__ __forceinline__ uint32_t bf2(float lo, float hi) {
+    const __nv_bfloat162 x = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&x);
+}
+template <bool INTER> __device__ __forceinline__ void close(const f2 *A, const f2 *B, uint4 &a, uint4 &b, __nv_bfloat16 *) {
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float x, y, z, t;
+        un(A[i], x, y);
+        un(B[i], z, t);
+        w[INTER ? 2 * i : i] = INTER ? bf2(x, z) : bf2(x, y);
+        w[INTER ? 2 * i + 1 : 4 + i] = INTER ? bf2(y, t) : bf2(z, t);
+    }
+    a = make_uint4(w[0], w[1], w[2], w[3]);
+    b = make_uint4(w[4], w[5], w[6], w[7]);
+}
+template <bool INTER> __device__ __forceinline__ void close(const f2 *A, const f2 *B, uint4 &a, uint4 &b, float *) {
+    float x[4], y[4];  // firsts, seconds
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        un(A[i], x[2 * i], x[2 * i + 1]);
+        un(B[i], y[2 * i], y[2 * i + 1]);
+    }
+    auto put = [](float p, float q, float r, float s) {
+        return make_uint4(__float_as_uint(p), __float_as_uint(q), __float_as_uint(r), __float_as_uint(s));
+    };
+    a = INTER ? put(x[0], y[0], x[1], y[1]) : put(x[0], x[1], x[2], x[3]);
+    b = INTER ? put(x[2], y[2], x[3], y[3]) : put(y[0], y[1], y[2], y[3]);
+}
 
 template <int LPT> __device__ __forceinline__ float sum_group(float x) {
 #pragma unroll
@@ -49,100 +145,107 @@ template <int LPT> __device__ __forceinline__ float sum_group(float x) {
     return x;
 }
 
-// cosines and sines of a lane's VEC angles at a position; turns: the lane's first in the table of
-// all of them, in turns per position
-template <int VEC, bool INTER>
-__device__ __forceinline__ void angles(int pos, const double *turns, int apart, bool turned, float *cs, float *sn) {
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-        cs[i] = 1.f;
-        sn[i] = 0.f;
-        if (turned) {
-            const double t = (double)pos * turns[INTER && i >= VEC / 2 ? apart + i : i];
-            sincospif(2.f * (float)(t - rint(t)), &sn[i], &cs[i]);
+// What all tokens share, in shared memory: inv_freq in turns per position (0 for channels that are
+// not turned) and both weights, in the order in which the lanes hold them.
+template <typename E, int D, bool INTER> struct Shared {
+    using L = Lay<E, D, INTER>;
+    static constexpr int VEC = L::VEC, LPT = L::LPT;
+    double turns[VEC][LPT];
+    float4 w[2][VEC / 2][LPT];  // firsts, then seconds
+
+    __device__ __forceinline__ void fill(const QkRope &p) {
+        for (int x = threadIdx.x; x < 2 * D; x += THREADS) {
+            const int which = x / D, at = x % D, j = at / (2 * VEC), i = at % (2 * VEC);
+            const L l(j, p.rot);
+            const int ch = l.channel(i >= VEC, i % VEC);
+            const float *src = which ? p.wk : p.wq;
+            reinterpret_cast<float *>(&w[which][i / 4][j])[i % 4] = src ? src[ch] : 1.f;
+            if (which == 0 && i < VEC) turns[i][j] = l.turned ? p.inv_freq[l.pair(i)] * INV_2PI : 0.0;
         }
+        __syncthreads();
+    }
+    __device__ __forceinline__ void weights(int which, int j, f2 *A, f2 *B) const {
+#pragma unroll
+        for (int i = 0; i < VEC / 4; ++i) {
+            const float4 u = w[which][i][j], v = w[which][VEC / 4 + i][j];
+            A[2 * i] = mk(u.x, u.y); A[2 * i + 1] = mk(u.z, u.w);
+            B[2 * i] = mk(v.x, v.y); B[2 * i + 1] = mk(v.z, v.w);
+        }
+    }
+    // cosines, sines and their negatives of a lane's angles.  fp32 results take sincospif (2 ulp); for
+    // bf16 the fast sine and cosine (off by 2^-20.9 at most on [-pi, pi]) are 2^-12 of a rounding, and
+    // a third of the forward's instructions fewer.
+    __device__ __forceinline__ void angles(int pos, int j, f2 *cs, f2 *sn, f2 *ns) const {
+        const double p = (double)pos;
+#pragma unroll
+        for (int i = 0; i < VEC; i += 2) {
+            float c[2], s[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const double t = p * turns[i + k][j];
+                const float f = (float)(t - rint(t));
+                if (sizeof(E) == 4) {
+                    sincospif(2.f * f, &s[k], &c[k]);
+                } else {
+                    s[k] = __sinf(6.28318530717958647692f * f);
+                    c[k] = __cosf(6.28318530717958647692f * f);
+                }
+            }
+            cs[i / 2] = mk(c[0], c[1]);
+            sn[i / 2] = mk(s[0], s[1]);
+            ns[i / 2] = mk(-s[0], -s[1]);
+        }
+    }
+};
+
+// (A, B) -> (A cos + B ns, B cos + A sn): turned forwards with ns = -sin, back with sin and -sin exchanged
+template <int N2> __device__ __forceinline__ void rotate(f2 *A, f2 *B, const f2 *cs, const f2 *sn, const f2 *ns) {
+#pragma unroll
+    for (int i = 0; i < N2; ++i) {
+        const f2 x = A[i], y = B[i];
+        A[i] = fma(x, cs[i], mul(y, ns[i]));
+        B[i] = fma(y, cs[i], mul(x, sn[i]));
     }
 }
 
-__device__ __forceinline__ void cp16(void *dst, const void *src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src)
-                 : "memory");
+__device__ __forceinline__ void cp16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+__device__ __forceinline__ uint4 lds16(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+    return v;
+}
 
 // The rows ahead of a lane: each lane copies the very vectors that it will use into a ring of its
 // own in shared memory (PF slots of NV vectors, a vector of the warp's 32 lanes side by side), so
 // that a warp has PF - 1 rows' loads in flight without holding them in registers, and no lane
 // waits for another.  A slot is filled again one row after its values were used.
 template <int NV, int PF> struct Ring {
-    uint4 *base;
-    int put = 0, got = 0;
-    static constexpr int WARP_BYTES = PF * NV * 32 * 16;
-    __device__ __forceinline__ Ring(char *smem) {
-        base = reinterpret_cast<uint4 *>(smem + (threadIdx.x >> 5) * WARP_BYTES) + (threadIdx.x & 31);
+    static constexpr int VECTOR = 32 * 16, SLOT = NV * VECTOR, WARP_BYTES = PF * SLOT;
+    uint32_t base, put, got;
+    __device__ __forceinline__ explicit Ring(char *smem) {
+        base = (uint32_t)__cvta_generic_to_shared(smem) + (threadIdx.x >> 5) * WARP_BYTES + (threadIdx.x & 31) * 16;
+        put = got = base;
     }
-    __device__ __forceinline__ uint4 *slot(int s, int v) { return base + (s * NV + v) * 32; }
     __device__ __forceinline__ void pushed() {
         cp_commit();
-        put = put + 1 == PF ? 0 : put + 1;
+        put = put == base + (PF - 1) * SLOT ? base : put + SLOT;
     }
-    __device__ __forceinline__ void popped() { got = got + 1 == PF ? 0 : got + 1; }
+    __device__ __forceinline__ void popped() { got = got == base + (PF - 1) * SLOT ? base : got + SLOT; }
+    static __device__ __forceinline__ void wait() { cp_wait<PF - 2>(); }
 };
-
-// rotates the pairs of (a, b) by the angles, or back (DIR = -1)
-template <int VEC, bool INTER, int DIR>
-__device__ __forceinline__ void rotate(float *a, float *b, const float *cs, const float *sn) {
-    if (INTER) {
-#pragma unroll
-        for (int i = 0; i < VEC / 2; ++i) {
-            const float c0 = cs[i], s0 = DIR * sn[i], c1 = cs[VEC / 2 + i], s1 = DIR * sn[VEC / 2 + i];
-            const float a0 = a[2 * i], a1 = a[2 * i + 1], b0 = b[2 * i], b1 = b[2 * i + 1];
-            a[2 * i] = a0 * c0 - a1 * s0;
-            a[2 * i + 1] = a1 * c0 + a0 * s0;
-            b[2 * i] = b0 * c1 - b1 * s1;
-            b[2 * i + 1] = b1 * c1 + b0 * s1;
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-            const float c = cs[i], s = DIR * sn[i], x = a[i], y = b[i];
-            a[i] = x * c - y * s;
-            b[i] = y * c + x * s;
-        }
-    }
-}
-
-template <typename E, int D>
-__device__ __forceinline__ void load_w(const float *w, const Lay<E, D> &l, float *wa, float *wb) {
-    constexpr int VEC = Lay<E, D>::VEC;
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-        wa[i] = w ? w[l.ia * VEC + i] : 1.f;
-        wb[i] = w ? w[l.ib * VEC + i] : 1.f;
-    }
-}
-
-// inv_freq in turns per position, for the whole CTA
-template <int D> __device__ __forceinline__ void fill_turns(double *turns, const QkRope &p) {
-    for (int i = threadIdx.x; i < p.rot / 2; i += THREADS) turns[i] = p.inv_freq[i] * INV_2PI;
-    __syncthreads();
-}
-// the lane's first angle in that table, and (interleaved) where its second vector's begin
-template <typename E, int D, bool INTER> __device__ __forceinline__ int first_turn(const Lay<E, D> &l, int j, int *apart) {
-    constexpr int VEC = Lay<E, D>::VEC;
-    *apart = (l.ib - l.ia) * (VEC / 2) - VEC / 2;
-    return INTER ? l.ia * (VEC / 2) : j * VEC;
-}
 
 // The heads are cut into chunks of hpg (blockIdx.y), so that a call of few tokens still has many
 // warps: a chunk [h0, h1) of the Hq + Hk (cache: + Hk values) heads.
 template <typename E, int D, bool INTER, bool CACHE>
 __global__ void __launch_bounds__(THREADS, 3) k_qkrope(const QkRope p, int hpg) {
-    using L = Lay<E, D>;
-    constexpr int VEC = L::VEC, LPT = L::LPT, TPW = L::TPW;
+    using L = Lay<E, D, INTER>;
+    constexpr int VEC = L::VEC, N2 = L::N2, LPT = L::LPT, TPW = L::TPW;
     extern __shared__ __align__(16) char ring_smem[];
-    __shared__ double turns[D / 2];
+    __shared__ Shared<E, D, INTER> sh;
     const int lane = threadIdx.x & 31, j = lane % LPT;
     const L l(j, p.rot);
     const int heads = p.Hq + p.Hk * (CACHE ? 2 : 1);
@@ -152,18 +255,29 @@ __global__ void __launch_bounds__(THREADS, 3) k_qkrope(const QkRope p, int hpg) 
 
     Ring<2, PF_FWD> ring(ring_smem);
     auto token = [&](size_t at) { return min(at + lane / LPT, p.N - 1); };  // behind the last: computed, not stored
-    size_t ln = n0;  // the row whose load is next
-    int lh = h0;
+    size_t ln = n0;               // the token whose row is copied next,
+    int lh = h0, left = 0;        // the head behind it, how many of the tensor's rows are left,
+    const E *src = nullptr;       // the row
     auto push = [&]() {
         if (ln < p.N) {
-            const size_t n = token(ln);
-            const E *src;
-            if (lh < p.Hq) src = (const E *)p.q + n * p.qs + lh * D;
-            else if (!CACHE || lh < p.Hq + p.Hk) src = (const E *)p.k + n * p.ks + (lh - p.Hq) * D;
-            else src = (const E *)p.v + n * p.vs + (lh - p.Hq - p.Hk) * D;
-            cp16(ring.slot(ring.put, 0), src + l.ia * VEC);
-            cp16(ring.slot(ring.put, 1), src + l.ib * VEC);
-            if (++lh == h1) {
+            if (left == 0) {  // the next tensor of the token
+                const size_t n = token(ln);
+                if (lh < p.Hq) {
+                    src = (const E *)p.q + n * p.qs + lh * D;
+                    left = min(h1, p.Hq) - lh;
+                } else if (!CACHE || lh < p.Hq + p.Hk) {
+                    src = (const E *)p.k + n * p.ks + (lh - p.Hq) * D;
+                    left = min(h1, p.Hq + p.Hk) - lh;
+                } else {
+                    src = (const E *)p.v + n * p.vs + (lh - p.Hq - p.Hk) * D;
+                    left = h1 - lh;
+                }
+                lh += left;
+            }
+            cp16(ring.put, src + l.ia * VEC);
+            cp16(ring.put + ring.VECTOR, src + l.ib * VEC);
+            src += D;
+            if (--left == 0 && lh == h1) {
                 lh = h0;
                 ln += step;
             }
@@ -172,14 +286,12 @@ __global__ void __launch_bounds__(THREADS, 3) k_qkrope(const QkRope p, int hpg) 
     };
 #pragma unroll
     for (int i = 0; i < PF_FWD - 1; ++i) push();
-    fill_turns<D>(turns, p);
-    int apart;
-    const double *mine = turns + first_turn<E, D, INTER>(l, j, &apart);
+    sh.fill(p);
     for (; n0 < p.N; n0 += step) {
         const bool act = n0 + lane / LPT < p.N;
         const size_t n = token(n0);
-        float cs[VEC], sn[VEC];
-        angles<VEC, INTER>(p.pos ? p.pos[n] : (int)(n % p.T), mine, apart, l.turned, cs, sn);
+        f2 cs[N2], sn[N2], ns[N2];
+        sh.angles(p.pos ? p.pos[n] : (int)(n % p.T), j, cs, sn, ns);
         E *qdst = (E *)p.qo + n * ((size_t)p.Hq * D), *kdst = nullptr, *vdst = nullptr;
         if (CACHE) {
             const long long slot = p.slots[n];
@@ -192,38 +304,48 @@ __global__ void __launch_bounds__(THREADS, 3) k_qkrope(const QkRope p, int hpg) 
             kdst = (E *)p.ko + n * ((size_t)p.Hk * D);
         }
         // heads [from, to) of one tensor, to dst, dense in the head
-        auto run = [&](E *dst, const float *w, int from, int to) {
+        auto run = [&](E *dst, int which, int from, int to) {
             if (from >= to) return;
-            float wa[VEC], wb[VEC];
-            load_w<E, D>(w, l, wa, wb);
-            for (int h = from; h < to; ++h) {
-                float a[VEC], b[VEC], ss = 0.f;
-                cp_wait<PF_FWD - 2>();
-                Vec<E, VEC>::ld(reinterpret_cast<const E *>(ring.slot(ring.got, 0)), a);
-                Vec<E, VEC>::ld(reinterpret_cast<const E *>(ring.slot(ring.got, 1)), b);
+            f2 wA[N2], wB[N2];
+            sh.weights(which, j, wA, wB);
+            const bool store = act && dst;
+            dst += from * D;
+#pragma unroll 1
+            for (int h = from; h < to; ++h, dst += D) {
+                f2 A[N2], B[N2], ss = 0;
+                ring.wait();
+                open<INTER>(lds16(ring.got), lds16(ring.got + ring.VECTOR), A, B, (E *)nullptr);
                 push();
                 ring.popped();
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) ss += a[i] * a[i] + b[i] * b[i];
-                const float r = rsqrtf(sum_group<LPT>(ss) * (1.f / D) + EPS);
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) {
-                    a[i] *= r * wa[i];
-                    b[i] *= r * wb[i];
+                for (int i = 0; i < N2; ++i) {
+                    ss = fma(A[i], A[i], ss);
+                    ss = fma(B[i], B[i], ss);
+                    A[i] = mul(A[i], wA[i]);
+                    B[i] = mul(B[i], wB[i]);
                 }
-                rotate<VEC, INTER, 1>(a, b, cs, sn);
-                if (act && dst) {
-                    Vec<E, VEC>::st(dst + h * D + l.ia * VEC, a);
-                    Vec<E, VEC>::st(dst + h * D + l.ib * VEC, b);
+                rotate<N2>(A, B, cs, sn, ns);
+                const float r = rsqrtf(sum_group<LPT>(sum2(ss)) * (1.f / D) + EPS);
+                const f2 rr = mk(r, r);
+#pragma unroll
+                for (int i = 0; i < N2; ++i) {
+                    A[i] = mul(A[i], rr);
+                    B[i] = mul(B[i], rr);
+                }
+                uint4 a, b;
+                close<INTER>(A, B, a, b, (E *)nullptr);
+                if (store) {
+                    *reinterpret_cast<uint4 *>(dst + l.ia * VEC) = a;
+                    *reinterpret_cast<uint4 *>(dst + l.ib * VEC) = b;
                 }
             }
         };
-        run(qdst, p.wq, min(h0, p.Hq), min(h1, p.Hq));
-        run(kdst, p.wk, max(h0 - p.Hq, 0), min(h1 - p.Hq, p.Hk));
+        run(qdst, 0, min(h0, p.Hq), min(h1, p.Hq));
+        run(kdst, 1, max(h0 - p.Hq, 0), min(h1 - p.Hq, p.Hk));
         if (CACHE) {
             for (int h = max(h0 - p.Hq - p.Hk, 0); h < h1 - p.Hq - p.Hk; ++h) {
-                cp_wait<PF_FWD - 2>();
-                const uint4 a = *ring.slot(ring.got, 0), b = *ring.slot(ring.got, 1);
+                ring.wait();
+                const uint4 a = lds16(ring.got), b = lds16(ring.got + ring.VECTOR);
                 push();
                 ring.popped();
                 if (act && vdst) {
@@ -238,12 +360,11 @@ __global__ void __launch_bounds__(THREADS, 3) k_qkrope(const QkRope p, int hpg) 
 // part (or null): [CTA][2][D], the CTA's sums of the weights' gradients (query, key)
 template <typename E, int D, bool INTER>
 __global__ void __launch_bounds__(THREADS, 2) k_qkrope_bwd(const QkRope p, int hpg) {
-    using L = Lay<E, D>;
-    constexpr int VEC = L::VEC, LPT = L::LPT, TPW = L::TPW, WARPS = THREADS / 32;
+    using L = Lay<E, D, INTER>;
+    constexpr int VEC = L::VEC, N2 = L::N2, LPT = L::LPT, TPW = L::TPW, WARPS = THREADS / 32;
     extern __shared__ __align__(16) char ring_smem[];
+    __shared__ Shared<E, D, INTER> sh;
     __shared__ float red[WARPS][2][D];
-    __shared__ double turns[D / 2];
-    __shared__ __align__(16) float wsh[2][D];  // the weights (in registers they would be spilled)
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, j = lane % LPT;
     const L l(j, p.rot);
     const int h0 = blockIdx.y * hpg, h1 = min(p.Hq + p.Hk, h0 + hpg);
@@ -253,18 +374,30 @@ __global__ void __launch_bounds__(THREADS, 2) k_qkrope_bwd(const QkRope p, int h
     Ring<4, PF_BWD> ring(ring_smem);
     auto token = [&](size_t at) { return min(at + lane / LPT, p.N - 1); };
     size_t ln = n0;
-    int lh = h0;
+    int lh = h0, left = 0;
+    const E *src = nullptr, *grad = nullptr;
     auto push = [&]() {
         if (ln < p.N) {
-            const size_t n = token(ln);
-            const bool isq = lh < p.Hq;
-            const E *x = isq ? (const E *)p.q + n * p.qs + lh * D : (const E *)p.k + n * p.ks + (lh - p.Hq) * D;
-            const E *g = isq ? (const E *)p.gq + (n * p.Hq + lh) * D : (const E *)p.gk + (n * p.Hk + lh - p.Hq) * D;
-            cp16(ring.slot(ring.put, 0), x + l.ia * VEC);
-            cp16(ring.slot(ring.put, 1), x + l.ib * VEC);
-            cp16(ring.slot(ring.put, 2), g + l.ia * VEC);
-            cp16(ring.slot(ring.put, 3), g + l.ib * VEC);
-            if (++lh == h1) {
+            if (left == 0) {
+                const size_t n = token(ln);
+                if (lh < p.Hq) {
+                    src = (const E *)p.q + n * p.qs + lh * D;
+                    grad = (const E *)p.gq + (n * p.Hq + lh) * D;
+                    left = min(h1, p.Hq) - lh;
+                } else {
+                    src = (const E *)p.k + n * p.ks + (lh - p.Hq) * D;
+                    grad = (const E *)p.gk + (n * p.Hk + lh - p.Hq) * D;
+                    left = h1 - lh;
+                }
+                lh += left;
+            }
+            cp16(ring.put, src + l.ia * VEC);
+            cp16(ring.put + ring.VECTOR, src + l.ib * VEC);
+            cp16(ring.put + 2 * ring.VECTOR, grad + l.ia * VEC);
+            cp16(ring.put + 3 * ring.VECTOR, grad + l.ib * VEC);
+            src += D;
+            grad += D;
+            if (--left == 0 && lh == h1) {
                 lh = h0;
                 ln += step;
             }
@@ -273,66 +406,75 @@ __global__ void __launch_bounds__(THREADS, 2) k_qkrope_bwd(const QkRope p, int h
     };
 #pragma unroll
     for (int i = 0; i < PF_BWD - 1; ++i) push();
-    for (int i = threadIdx.x; i < 2 * D; i += THREADS) {
-        const float *w = i < D ? p.wq : p.wk;
-        wsh[i / D][i % D] = w ? w[i % D] : 1.f;
-    }
-    fill_turns<D>(turns, p);
-    int apart;
-    const double *mine = turns + first_turn<E, D, INTER>(l, j, &apart);
-    float dwq[2 * VEC] = {}, dwk[2 * VEC] = {};
+    sh.fill(p);
+    f2 dwq[2 * N2] = {}, dwk[2 * N2] = {};  // firsts, then seconds
     for (; n0 < p.N; n0 += step) {
         const bool act = n0 + lane / LPT < p.N;
         const size_t n = token(n0);
-        float cs[VEC], sn[VEC];
-        angles<VEC, INTER>(p.pos ? p.pos[n] : (int)(n % p.T), mine, apart, l.turned, cs, sn);
-        auto run = [&](E *dst, const float *w, float *dw, int from, int to) {
-            for (int h = from; h < to; ++h) {
-                float a[VEC], b[VEC], ga[VEC], gb[VEC], ss = 0.f, sg = 0.f;
-                cp_wait<PF_BWD - 2>();
-                Vec<E, VEC>::ld(reinterpret_cast<const E *>(ring.slot(ring.got, 0)), a);
-                Vec<E, VEC>::ld(reinterpret_cast<const E *>(ring.slot(ring.got, 1)), b);
-                Vec<E, VEC>::ld(reinterpret_cast<const E *>(ring.slot(ring.got, 2)), ga);
-                Vec<E, VEC>::ld(reinterpret_cast<const E *>(ring.slot(ring.got, 3)), gb);
+        f2 cs[N2], sn[N2], ns[N2];
+        sh.angles(p.pos ? p.pos[n] : (int)(n % p.T), j, cs, sn, ns);
+        auto run = [&](E *dst, int which, f2 *dw, int from, int to) {
+            dst += from * D;
+#pragma unroll 1
+            for (int h = from; h < to; ++h, dst += D) {
+                f2 A[N2], B[N2], gA[N2], gB[N2], ss = 0, sg = 0;
+                ring.wait();
+                open<INTER>(lds16(ring.got + 2 * ring.VECTOR), lds16(ring.got + 3 * ring.VECTOR), gA, gB, (E *)nullptr);
+                open<INTER>(lds16(ring.got), lds16(ring.got + ring.VECTOR), A, B, (E *)nullptr);
                 push();
                 ring.popped();
-                rotate<VEC, INTER, -1>(ga, gb, cs, sn);
+                rotate<N2>(gA, gB, cs, ns, sn);  // back
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) {
-                    ss += a[i] * a[i] + b[i] * b[i];
-                    sg += a[i] * (ga[i] * w[l.ia * VEC + i]) + b[i] * (gb[i] * w[l.ib * VEC + i]);
+                for (int i = 0; i < N2; ++i) {
+                    ss = fma(A[i], A[i], ss);
+                    ss = fma(B[i], B[i], ss);
                 }
-                const float r = rsqrtf(sum_group<LPT>(ss) * (1.f / D) + EPS);
-                const float c = sum_group<LPT>(sg) * (1.f / D) * r * r;  // mean(g w n) / r, n = x r
-                if (act) {
+                const float r = rsqrtf(sum_group<LPT>(sum2(ss)) * (1.f / D) + EPS);
+                const float rl = act ? r : 0.f;  // a group behind the last token adds nothing
+                const f2 rr = mk(rl, rl);
+                f2 wA[N2], wB[N2];
+                sh.weights(which, j, wA, wB);
 #pragma unroll
-                    for (int i = 0; i < VEC; ++i) {
-                        dw[i] += ga[i] * (a[i] * r);
-                        dw[VEC + i] += gb[i] * (b[i] * r);
-                        a[i] = r * (ga[i] * w[l.ia * VEC + i] - a[i] * c);
-                        b[i] = r * (gb[i] * w[l.ib * VEC + i] - b[i] * c);
-                    }
-                    Vec<E, VEC>::st(dst + h * D + l.ia * VEC, a);
-                    Vec<E, VEC>::st(dst + h * D + l.ib * VEC, b);
+                for (int i = 0; i < N2; ++i) {  // x to n = x r, dw += g n, g to g w
+                    A[i] = mul(A[i], rr);
+                    B[i] = mul(B[i], rr);
+                    dw[i] = fma(gA[i], A[i], dw[i]);
+                    dw[N2 + i] = fma(gB[i], B[i], dw[N2 + i]);
+                    gA[i] = mul(gA[i], wA[i]);
+                    gB[i] = mul(gB[i], wB[i]);
+                    sg = fma(gA[i], A[i], sg);
+                    sg = fma(gB[i], B[i], sg);
+                }
+                const float c = sum_group<LPT>(sum2(sg)) * (-1.f / D);  // - mean(g w n)
+                const f2 cc = mk(c, c);
+#pragma unroll
+                for (int i = 0; i < N2; ++i) {
+                    gA[i] = mul(fma(A[i], cc, gA[i]), rr);
+                    gB[i] = mul(fma(B[i], cc, gB[i]), rr);
+                }
+                uint4 a, b;
+                close<INTER>(gA, gB, a, b, (E *)nullptr);
+                if (act) {
+                    *reinterpret_cast<uint4 *>(dst + l.ia * VEC) = a;
+                    *reinterpret_cast<uint4 *>(dst + l.ib * VEC) = b;
                 }
             }
         };
-        run((E *)p.dq + n * p.dqs, wsh[0], dwq, min(h0, p.Hq), min(h1, p.Hq));
-        run((E *)p.dk + n * p.dks, wsh[1], dwk, max(h0 - p.Hq, 0), min(h1 - p.Hq, p.Hk));
+        run((E *)p.dq + n * p.dqs, 0, dwq, min(h0, p.Hq), min(h1, p.Hq));
+        run((E *)p.dk + n * p.dks, 1, dwk, max(h0 - p.Hq, 0), min(h1 - p.Hq, p.Hk));
     }
     if (!p.part) return;
     // over the warp's tokens, then over the warps in order
 #pragma unroll
-    for (int i = 0; i < 2 * VEC; ++i) {
+    for (int i = 0; i < 2 * N2; ++i) {
+        float x[4];
+        un(dwq[i], x[0], x[1]);
+        un(dwk[i], x[2], x[3]);
 #pragma unroll
-        for (int o = LPT; o < 32; o <<= 1) {
-            dwq[i] += __shfl_xor_sync(0xffffffffu, dwq[i], o);
-            dwk[i] += __shfl_xor_sync(0xffffffffu, dwk[i], o);
-        }
-        if (lane < LPT) {
-            const int at = (i < VEC ? l.ia * VEC + i : l.ib * VEC + i - VEC);
-            red[warp][0][at] = dwq[i];
-            red[warp][1][at] = dwk[i];
+        for (int k = 0; k < 4; ++k) {
+#pragma unroll
+            for (int o = LPT; o < 32; o <<= 1) x[k] += __shfl_xor_sync(0xffffffffu, x[k], o);
+            if (lane < LPT) red[warp][k >> 1][l.channel(i >= N2, 2 * (i % N2) + (k & 1))] = x[k];
         }
     }
     __syncthreads();
@@ -380,7 +522,7 @@ static Grid plan(size_t N, int heads, int tpw, size_t max_ctas) {
 
 template <typename E, int D, bool INTER> static cudaError_t fwd(const QkRope &p, cudaStream_t s) {
     const bool cache = p.slots != nullptr;
-    const Grid g = plan(p.N, p.Hq + p.Hk * (cache ? 2 : 1), Lay<E, D>::TPW, FWD_CTAS);
+    const Grid g = plan(p.N, p.Hq + p.Hk * (cache ? 2 : 1), Lay<E, D, INTER>::TPW, FWD_CTAS);
     auto go = [&](auto kern) -> cudaError_t {
         constexpr int smem = Ring<2, PF_FWD>::WARP_BYTES * (THREADS / 32);
         const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
@@ -392,7 +534,7 @@ template <typename E, int D, bool INTER> static cudaError_t fwd(const QkRope &p,
 }
 
 template <typename E, int D, bool INTER> static cudaError_t bwd(const QkRope &p, cudaStream_t s) {
-    const Grid g = plan(p.N, p.Hq + p.Hk, Lay<E, D>::TPW, BWD_CTAS);
+    const Grid g = plan(p.N, p.Hq + p.Hk, Lay<E, D, INTER>::TPW, BWD_CTAS);
     constexpr int smem = Ring<4, PF_BWD>::WARP_BYTES * (THREADS / 32);
     const cudaError_t e = cudaFuncSetAttribute(k_qkrope_bwd<E, D, INTER>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
