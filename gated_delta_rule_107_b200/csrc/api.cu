@@ -871,7 +871,7 @@ static int check_qkrope(int B, int T, int Hq, int Hk, int d, int rot, int interl
     const int rc = check_rows(B, T, 1, d, dtype, &rows);
     if (rc != DR_OK) return rc;
     if (Hq < 0 || Hk < 0 || rot < 0 || rot > d || (interleaved != 0 && interleaved != 1)) return DR_ERR_ARG;
-    if (Hq > 1024 || Hk > 1024 || Hq + Hk > 1024 || rot % 16 != 0) return DR_ERR_UNSUPPORTED;
+    if (Hq > 1024 || Hk > 1024 || Hq + Hk > 1024 || rot % 16 != 0 || rows > INT_MAX) return DR_ERR_UNSUPPORTED;
     if ((Hq > 0 && !q) || (Hk > 0 && !k) || (rot > 0 && !inv_freq)) return rows == 0 ? DR_OK : DR_ERR_ARG;
     int sc = Hq > 0 ? check_stride(q_stride, (long long)Hq * d, dtype) : DR_OK;
     if (sc == DR_OK && Hk > 0) sc = check_stride(k_stride, (long long)Hk * d, dtype);

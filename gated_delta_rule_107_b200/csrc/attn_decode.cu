@@ -717,17 +717,8 @@ template <class C, int D> static cudaError_t launch(Args x, cudaStream_t s) {
     k_attn<C, D><<<ctas, THREADS, smem, s>>>(x);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    // launched while k_attn runs, so that only its work follows (2 us less on the smallest calls)
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3(ctas, x.G < C::GB ? x.G : C::GB);
-    cfg.blockDim = dim3(256);
-    cfg.stream = s;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k_attn_join<typename C::E, D>, x);
+    // set up while k_attn runs, so that only its work follows (2 us less on the smallest calls)
+    return launch_after(k_attn_join<typename C::E, D>, dim3(ctas, x.G < C::GB ? x.G : C::GB), dim3(256), s, x);
 }
 
 static int heads_per_block(int G, bool bf16) {

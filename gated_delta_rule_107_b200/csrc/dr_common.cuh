@@ -77,6 +77,22 @@ struct Tensors {
     void *y;
 };
 
+// Launches a kernel that begins with griddepcontrol.wait behind one that begins with
+// griddepcontrol.launch_dependents: it is set up while that one runs and waits for its end.
+template <typename... P, typename... A>
+inline cudaError_t launch_after(void (*kern)(P...), dim3 grid, dim3 block, cudaStream_t s, A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, P(args)...);
+}
+
 // Optional launch timing: records ev[i] on the stream just before kernel launch i
 // and ev[n_launches] after the last one (the *_timed entry points).  Inactive
 // when ev is null.

@@ -24,8 +24,9 @@ namespace qkr {
 
 constexpr float EPS = 1e-6f;
 constexpr int THREADS = 256;
-constexpr int PF_FWD = 5, PF_BWD = 5;  // slots of the rows ahead
-constexpr int FWD_CTAS = 148 * 64, BWD_CTAS = 1184;  // at most; the backward's are also its partial sums
+constexpr int PF_FWD = 5, PF_BWD = 3;  // slots of the rows ahead
+constexpr long long WARPS_WANTED = 16 * 148;
+constexpr int BWD_CTAS = 2 * 148;         // one wave; they are also the number of its partial sums
 constexpr double INV_2PI = 0.15915494309189533577;
 
 // Two fp32 numbers in a 64-bit register pair: Blackwell's packed arithmetic takes one issue slot
@@ -47,6 +48,11 @@ __device__ __forceinline__ f2 fma(f2 a, f2 b, f2 c) {
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
     return d;
 }
+__device__ __forceinline__ f2 sub(f2 a, f2 b) {
+    f2 d;
+    asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
 __device__ __forceinline__ float sum2(f2 x) {
     float a, b;
     un(x, a, b);
@@ -65,8 +71,8 @@ template <typename E, int D, bool INTER> struct Lay {
     __device__ __forceinline__ Lay(int j_, int rot) : j(j_) {
         const int half = rot / (2 * VEC);
         turned = j < half;
-        ia = turned ? j : 2 * j;
-        ib = turned ? j + half : 2 * j + 1;
+        ia = turned ? j : j + half;  // neighbouring lanes hold neighbouring vectors
+        ib = turned ? j + half : j + LPT;
     }
     // the channel of the i-th first (0) or second (1) number
     __device__ __forceinline__ int channel(int second, int i) const {
@@ -172,10 +178,10 @@ template <typename E, int D, bool INTER> struct Shared {
             B[2 * i] = mk(v.x, v.y); B[2 * i + 1] = mk(v.z, v.w);
         }
     }
-    // cosines, sines and their negatives of a lane's angles.  fp32 results take sincospif (2 ulp); for
+    // cosines and sines of a lane's angles.  fp32 results take sincospif (2 ulp); for
     // bf16 the fast sine and cosine (off by 2^-20.9 at most on [-pi, pi]) are 2^-12 of a rounding, and
     // a third of the forward's instructions fewer.
-    __device__ __forceinline__ void angles(int pos, int j, f2 *cs, f2 *sn, f2 *ns) const {
+    __device__ __forceinline__ void angles(int pos, int j, f2 *cs, f2 *sn) const {
         const double p = (double)pos;
 #pragma unroll
         for (int i = 0; i < VEC; i += 2) {
@@ -193,18 +199,22 @@ template <typename E, int D, bool INTER> struct Shared {
             }
             cs[i / 2] = mk(c[0], c[1]);
             sn[i / 2] = mk(s[0], s[1]);
-            ns[i / 2] = mk(-s[0], -s[1]);
         }
     }
 };
 
-// (A, B) -> (A cos + B ns, B cos + A sn): turned forwards with ns = -sin, back with sin and -sin exchanged
-template <int N2> __device__ __forceinline__ void rotate(f2 *A, f2 *B, const f2 *cs, const f2 *sn, const f2 *ns) {
+// (A, B) -> (A cos - B sin, B cos + A sin), or BACK
+template <int N2, bool BACK> __device__ __forceinline__ void rotate(f2 *A, f2 *B, const f2 *cs, const f2 *sn) {
 #pragma unroll
     for (int i = 0; i < N2; ++i) {
         const f2 x = A[i], y = B[i];
-        A[i] = fma(x, cs[i], mul(y, ns[i]));
-        B[i] = fma(y, cs[i], mul(x, sn[i]));
+        if (BACK) {
+            A[i] = fma(x, cs[i], mul(y, sn[i]));
+            B[i] = sub(mul(y, cs[i]), mul(x, sn[i]));
+        } else {
+            A[i] = sub(mul(x, cs[i]), mul(y, sn[i]));
+            B[i] = fma(y, cs[i], mul(x, sn[i]));
+        }
     }
 }
 
@@ -250,16 +260,16 @@ __global__ void __launch_bounds__(THREADS, 3) k_qkrope(const QkRope p, int hpg) 
     const L l(j, p.rot);
     const int heads = p.Hq + p.Hk * (CACHE ? 2 : 1);
     const int h0 = blockIdx.y * hpg, h1 = min(heads, h0 + hpg);
-    const size_t step = (size_t)gridDim.x * (THREADS / 32) * TPW;
-    size_t n0 = ((size_t)blockIdx.x * (THREADS / 32) + (threadIdx.x >> 5)) * TPW;
+    const unsigned N = (unsigned)p.N, step = gridDim.x * (THREADS / 32) * TPW;  // N < 2^31: no sum wraps
+    unsigned n0 = (blockIdx.x * (THREADS / 32) + (threadIdx.x >> 5)) * TPW;
 
     Ring<2, PF_FWD> ring(ring_smem);
-    auto token = [&](size_t at) { return min(at + lane / LPT, p.N - 1); };  // behind the last: computed, not stored
-    size_t ln = n0;               // the token whose row is copied next,
+    auto token = [&](unsigned at) { return (size_t)min(at + lane / LPT, N - 1); };  // behind the last: computed, not stored
+    unsigned ln = n0;               // the token whose row is copied next,
     int lh = h0, left = 0;        // the head behind it, how many of the tensor's rows are left,
     const E *src = nullptr;       // the row
     auto push = [&]() {
-        if (ln < p.N) {
+        if (ln < N) {
             if (left == 0) {  // the next tensor of the token
                 const size_t n = token(ln);
                 if (lh < p.Hq) {
@@ -287,22 +297,11 @@ __global__ void __launch_bounds__(THREADS, 3) k_qkrope(const QkRope p, int hpg) 
 #pragma unroll
     for (int i = 0; i < PF_FWD - 1; ++i) push();
     sh.fill(p);
-    for (; n0 < p.N; n0 += step) {
-        const bool act = n0 + lane / LPT < p.N;
+    for (; n0 < N; n0 += step) {
+        const bool act = n0 + lane / LPT < N;
         const size_t n = token(n0);
-        f2 cs[N2], sn[N2], ns[N2];
-        sh.angles(p.pos ? p.pos[n] : (int)(n % p.T), j, cs, sn, ns);
-        E *qdst = (E *)p.qo + n * ((size_t)p.Hq * D), *kdst = nullptr, *vdst = nullptr;
-        if (CACHE) {
-            const long long slot = p.slots[n];
-            if (slot >= 0 && slot < p.n_slots) {
-                const long long pg = slot / p.page, in = slot - pg * p.page;
-                kdst = (E *)p.kc + pg * p.kps + in * ((long long)p.Hk * D);
-                vdst = (E *)p.vc + pg * p.vps + in * ((long long)p.Hk * D);
-            }
-        } else {
-            kdst = (E *)p.ko + n * ((size_t)p.Hk * D);
-        }
+        f2 cs[N2], sn[N2];
+        sh.angles(p.pos ? p.pos[n] : (int)((unsigned)n % (unsigned)p.T), j, cs, sn);
         // heads [from, to) of one tensor, to dst, dense in the head
         auto run = [&](E *dst, int which, int from, int to) {
             if (from >= to) return;
@@ -324,7 +323,7 @@ __global__ void __launch_bounds__(THREADS, 3) k_qkrope(const QkRope p, int hpg) 
                     A[i] = mul(A[i], wA[i]);
                     B[i] = mul(B[i], wB[i]);
                 }
-                rotate<N2>(A, B, cs, sn, ns);
+                rotate<N2, false>(A, B, cs, sn);
                 const float r = rsqrtf(sum_group<LPT>(sum2(ss)) * (1.f / D) + EPS);
                 const f2 rr = mk(r, r);
 #pragma unroll
@@ -340,7 +339,16 @@ __global__ void __launch_bounds__(THREADS, 3) k_qkrope(const QkRope p, int hpg) 
                 }
             }
         };
-        run(qdst, 0, min(h0, p.Hq), min(h1, p.Hq));
+        run((E *)p.qo + n * ((size_t)p.Hq * D), 0, min(h0, p.Hq), min(h1, p.Hq));
+        E *kdst = CACHE ? nullptr : (E *)p.ko + n * ((size_t)p.Hk * D), *vdst = nullptr;
+        if (CACHE) {
+            const long long slot = p.slots[n];
+            if (slot >= 0 && slot < p.n_slots) {
+                const long long pg = slot / p.page, in = slot - pg * p.page;
+                kdst = (E *)p.kc + pg * p.kps + in * ((long long)p.Hk * D);
+                vdst = (E *)p.vc + pg * p.vps + in * ((long long)p.Hk * D);
+            }
+        }
         run(kdst, 1, max(h0 - p.Hq, 0), min(h1 - p.Hq, p.Hk));
         if (CACHE) {
             for (int h = max(h0 - p.Hq - p.Hk, 0); h < h1 - p.Hq - p.Hk; ++h) {
@@ -357,9 +365,23 @@ __global__ void __launch_bounds__(THREADS, 3) k_qkrope(const QkRope p, int hpg) 
     }
 }
 
+// The rows of TPW tokens side by side are a warp's item: TPW tokens x one head.  The items, head by head and then on to the next tokens, are one list cut
+// into runs of `per`, one a warp, which may begin and end inside the heads of its tokens.
+template <int TPW> struct Items {
+    unsigned tok;    // the first of the current tokens
+    int head, heads, todo;
+    __device__ __forceinline__ Items(const QkRope &p, int h, long long per) : heads(h) {
+        const long long all = (long long)((p.N + TPW - 1) / TPW) * h;
+        const long long first = ((long long)blockIdx.x * (THREADS / 32) + (threadIdx.x >> 5)) * per;
+        todo = (int)max(0ll, min(per, all - first));
+        tok = (unsigned)(first / h) * TPW;
+        head = (int)(first % h);
+    }
+};
+
 // part (or null): [CTA][2][D], the CTA's sums of the weights' gradients (query, key)
 template <typename E, int D, bool INTER>
-__global__ void __launch_bounds__(THREADS, 2) k_qkrope_bwd(const QkRope p, int hpg) {
+__global__ void __launch_bounds__(THREADS, 2) k_qkrope_bwd(const QkRope p, long long per) {
     using L = Lay<E, D, INTER>;
     constexpr int VEC = L::VEC, N2 = L::N2, LPT = L::LPT, TPW = L::TPW, WARPS = THREADS / 32;
     extern __shared__ __align__(16) char ring_smem[];
@@ -367,29 +389,34 @@ __global__ void __launch_bounds__(THREADS, 2) k_qkrope_bwd(const QkRope p, int h
     __shared__ float red[WARPS][2][D];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, j = lane % LPT;
     const L l(j, p.rot);
-    const int h0 = blockIdx.y * hpg, h1 = min(p.Hq + p.Hk, h0 + hpg);
-    const size_t step = (size_t)gridDim.x * WARPS * TPW;
-    size_t n0 = ((size_t)blockIdx.x * WARPS + warp) * TPW;
+    Items<TPW> now(p, p.Hq + p.Hk, per);
 
+    asm volatile("griddepcontrol.launch_dependents;");
     Ring<4, PF_BWD> ring(ring_smem);
-    auto token = [&](size_t at) { return min(at + lane / LPT, p.N - 1); };
-    size_t ln = n0;
-    int lh = h0, left = 0;
+    const unsigned N = (unsigned)p.N;
+    auto token = [&](unsigned at) { return (size_t)min(at + lane / LPT, N - 1); };
+    Items<TPW> next = now;
+    int left = 0;
     const E *src = nullptr, *grad = nullptr;
     auto push = [&]() {
-        if (ln < p.N) {
+        if (next.todo > 0) {
             if (left == 0) {
-                const size_t n = token(ln);
-                if (lh < p.Hq) {
-                    src = (const E *)p.q + n * p.qs + lh * D;
-                    grad = (const E *)p.gq + (n * p.Hq + lh) * D;
-                    left = min(h1, p.Hq) - lh;
+                const size_t n = token(next.tok);
+                const int h = next.head;
+                if (h < p.Hq) {
+                    src = (const E *)p.q + n * p.qs + h * D;
+                    grad = (const E *)p.gq + (n * p.Hq + h) * D;
+                    left = p.Hq - h;
                 } else {
-                    src = (const E *)p.k + n * p.ks + (lh - p.Hq) * D;
-                    grad = (const E *)p.gk + (n * p.Hk + lh - p.Hq) * D;
-                    left = h1 - lh;
+                    src = (const E *)p.k + n * p.ks + (h - p.Hq) * D;
+                    grad = (const E *)p.gk + (n * p.Hk + h - p.Hq) * D;
+                    left = next.heads - h;
                 }
-                lh += left;
+                next.head += left;
+                if (next.head == next.heads) {
+                    next.head = 0;
+                    next.tok += TPW;
+                }
             }
             cp16(ring.put, src + l.ia * VEC);
             cp16(ring.put + ring.VECTOR, src + l.ib * VEC);
@@ -397,10 +424,8 @@ __global__ void __launch_bounds__(THREADS, 2) k_qkrope_bwd(const QkRope p, int h
             cp16(ring.put + 3 * ring.VECTOR, grad + l.ib * VEC);
             src += D;
             grad += D;
-            if (--left == 0 && lh == h1) {
-                lh = h0;
-                ln += step;
-            }
+            --left;
+            --next.todo;
         }
         ring.pushed();
     };
@@ -408,11 +433,12 @@ __global__ void __launch_bounds__(THREADS, 2) k_qkrope_bwd(const QkRope p, int h
     for (int i = 0; i < PF_BWD - 1; ++i) push();
     sh.fill(p);
     f2 dwq[2 * N2] = {}, dwk[2 * N2] = {};  // firsts, then seconds
-    for (; n0 < p.N; n0 += step) {
-        const bool act = n0 + lane / LPT < p.N;
-        const size_t n = token(n0);
-        f2 cs[N2], sn[N2], ns[N2];
-        sh.angles(p.pos ? p.pos[n] : (int)(n % p.T), j, cs, sn, ns);
+    while (now.todo > 0) {
+        const bool act = now.tok + lane / LPT < N;
+        const size_t n = token(now.tok);
+        const int h0 = now.head, h1 = min(now.heads, h0 + now.todo);
+        f2 cs[N2], sn[N2];
+        sh.angles(p.pos ? p.pos[n] : (int)((unsigned)n % (unsigned)p.T), j, cs, sn);
         auto run = [&](E *dst, int which, f2 *dw, int from, int to) {
             dst += from * D;
 #pragma unroll 1
@@ -423,7 +449,7 @@ __global__ void __launch_bounds__(THREADS, 2) k_qkrope_bwd(const QkRope p, int h
                 open<INTER>(lds16(ring.got), lds16(ring.got + ring.VECTOR), A, B, (E *)nullptr);
                 push();
                 ring.popped();
-                rotate<N2>(gA, gB, cs, ns, sn);  // back
+                rotate<N2, true>(gA, gB, cs, sn);
 #pragma unroll
                 for (int i = 0; i < N2; ++i) {
                     ss = fma(A[i], A[i], ss);
@@ -462,6 +488,9 @@ __global__ void __launch_bounds__(THREADS, 2) k_qkrope_bwd(const QkRope p, int h
         };
         run((E *)p.dq + n * p.dqs, 0, dwq, min(h0, p.Hq), min(h1, p.Hq));
         run((E *)p.dk + n * p.dks, 1, dwk, max(h0 - p.Hq, 0), min(h1 - p.Hq, p.Hk));
+        now.todo -= h1 - h0;
+        now.head = 0;
+        now.tok += TPW;
     }
     if (!p.part) return;
     // over the warp's tokens, then over the warps in order
@@ -478,18 +507,18 @@ __global__ void __launch_bounds__(THREADS, 2) k_qkrope_bwd(const QkRope p, int h
         }
     }
     __syncthreads();
-    const size_t cta = (size_t)blockIdx.y * gridDim.x + blockIdx.x;
     for (int x = threadIdx.x; x < 2 * D; x += THREADS) {
         float s = 0.f;
 #pragma unroll
         for (int w = 0; w < WARPS; ++w) s += (&red[w][0][0])[x];
-        p.part[cta * 2 * D + x] = s;
+        p.part[(size_t)blockIdx.x * 2 * D + x] = s;
     }
 }
 
 // dwq, dwk = the partials' sums in order: 32 columns a CTA, 32 partials at a time
 template <int D> __global__ void __launch_bounds__(1024) k_qkrope_dw(const float *part, int n, float *dwq, float *dwk) {
     __shared__ float red[32][33];
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // launched while the partials are being formed
     const int cx = threadIdx.x & 31, ry = threadIdx.x >> 5, col = blockIdx.x * 32 + cx;
     float s = 0.f;
     for (int r = ry; r < n; r += 32) s += part[(size_t)r * 2 * D + col];
@@ -506,43 +535,41 @@ template <int D> __global__ void __launch_bounds__(1024) k_qkrope_dw(const float
     }
 }
 
-// Grid: tokens over x, head chunks over y.  The heads are only cut when whole tokens would leave
-// the GPU short of warps (16 an SM).
-struct Grid {
-    dim3 grid;
-    int hpg;
-};
-static Grid plan(size_t N, int heads, int tpw, size_t max_ctas) {
-    const size_t warps = (N + tpw - 1) / tpw, want = 148 * 16;
-    const int chunks = (int)min((size_t)heads, max((size_t)1, want / max((size_t)1, warps)));
-    const int hpg = (heads + chunks - 1) / chunks, ny = (heads + hpg - 1) / hpg;
-    const size_t nx = min((warps + THREADS / 32 - 1) / (THREADS / 32), max((size_t)1, max_ctas / ny));
-    return {dim3((unsigned)nx, (unsigned)ny), hpg};
-}
-
 template <typename E, int D, bool INTER> static cudaError_t fwd(const QkRope &p, cudaStream_t s) {
+    // A warp's tokens with all their heads, and as many CTAs as that gives, which the hardware deals
+    // out as others end (8 x 4096 tokens: 31.2 us; one wave of CTAs with equal runs of rows 33.0).
+    // Where that leaves the GPU short of 16 warps an SM, the heads are cut.
     const bool cache = p.slots != nullptr;
-    const Grid g = plan(p.N, p.Hq + p.Hk * (cache ? 2 : 1), Lay<E, D, INTER>::TPW, FWD_CTAS);
+    constexpr int TPW = Lay<E, D, INTER>::TPW, WARPS = THREADS / 32;
+    const long long heads = p.Hq + p.Hk * (cache ? 2 : 1), groups = (long long)((p.N + TPW - 1) / TPW);
+    const long long chunks = max(1ll, min(heads, WARPS_WANTED / groups));
+    const int hpg = (int)((heads + chunks - 1) / chunks);
+    const dim3 grid((unsigned)min((groups + WARPS - 1) / WARPS, 1ll << 20), (unsigned)((heads + hpg - 1) / hpg));
     auto go = [&](auto kern) -> cudaError_t {
         constexpr int smem = Ring<2, PF_FWD>::WARP_BYTES * (THREADS / 32);
         const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
-        kern<<<g.grid, THREADS, smem, s>>>(p, g.hpg);
+        kern<<<grid, THREADS, smem, s>>>(p, hpg);
         return cudaGetLastError();
     };
     return cache ? go(k_qkrope<E, D, INTER, true>) : go(k_qkrope<E, D, INTER, false>);
 }
 
 template <typename E, int D, bool INTER> static cudaError_t bwd(const QkRope &p, cudaStream_t s) {
-    const Grid g = plan(p.N, p.Hq + p.Hk, Lay<E, D, INTER>::TPW, BWD_CTAS);
+    // one wave of CTAs with equal runs: each CTA's sums of the weights' gradients cost it a reduction
+    // (8 x 4096 tokens: 46.4 us; a warp for every tokens' heads, 1024 CTAs, 53.5)
+    constexpr int TPW = Lay<E, D, INTER>::TPW, WARPS = BWD_CTAS * (THREADS / 32);
+    const long long items = (long long)((p.N + TPW - 1) / TPW) * (p.Hq + p.Hk), per = (items + WARPS - 1) / WARPS;
+    const int ctas = (int)((items + per * (THREADS / 32) - 1) / (per * (THREADS / 32)));
     constexpr int smem = Ring<4, PF_BWD>::WARP_BYTES * (THREADS / 32);
     const cudaError_t e = cudaFuncSetAttribute(k_qkrope_bwd<E, D, INTER>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     QkRope a = p;
     if (!p.dwq && !p.dwk) a.part = nullptr;
-    k_qkrope_bwd<E, D, INTER><<<g.grid, THREADS, smem, s>>>(a, g.hpg);
-    if (a.part) k_qkrope_dw<D><<<2 * D / 32, 1024, 0, s>>>(a.part, (int)(g.grid.x * g.grid.y), p.dwq, p.dwk);
-    return cudaGetLastError();
+    k_qkrope_bwd<E, D, INTER><<<ctas, THREADS, smem, s>>>(a, per);
+    const cudaError_t e2 = cudaGetLastError();
+    if (e2 != cudaSuccess || !a.part) return e2;
+    return launch_after(k_qkrope_dw<D>, dim3(2 * D / 32), dim3(1024), s, (const float *)a.part, ctas, p.dwq, p.dwk);
 }
 
 template <typename F> static cudaError_t by_type(const QkRope &p, bool bf16, F f) {

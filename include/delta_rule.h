@@ -424,7 +424,7 @@ int delta_rule_pages(const int *cached, const int *fresh, const int *free_pages,
  * precision.  q [B,T,Hq,d] and k [B,T,Hk,d] may be slices of one projection:
  * q_stride, k_stride are the elements from a token to the next (>= heads * d, a
  * multiple of 16 bytes), a token's heads are dense.  q_out, k_out are dense.
- * Hq or Hk may be 0 (its pointers are then unused); Hq + Hk <= 1024.
+ * Hq or Hk may be 0 (its pointers are then unused); Hq + Hk <= 1024, B * T < 2^31.
  *
  * delta_rule_qkrope_bwd: for dq_out, dk_out (dense), the gradients dq, dk_ of q
  * and k (token strides dq_stride, dk_stride) and dwq, dwk [d] fp32, the sums
