@@ -1,6 +1,7 @@
 """ctypes binding of libdeltarule.so (the C ABI in include/delta_rule.h).
 
-Argument marshalling only: every step of the computation runs in the library's
+Argument marshalling only (for the softmax-attention layers' calls it is done in C++,
+csrc/torch_calls.cpp): every step of the computation runs in the library's
 CUDA kernels.  PyTorch supplies device memory and the current stream.  There is
 no fallback: if the shared library is missing or a call fails, an exception is
 raised.
@@ -30,7 +31,6 @@ The ``for_bwd`` argument of ``workspace_size`` and ``launches`` names the call:
 from __future__ import annotations
 
 import ctypes
-import functools
 import math
 import os
 
@@ -610,73 +610,33 @@ def attn_decode_raw(*args) -> int:
     return load().delta_rule_attn_decode(*args)
 
 
-def _refuse(t, what, dtype, dev, shape):
-    if t.dtype is not dtype or t.device != dev:
-        raise ValueError(f"{what}: expected {dtype} on {dev}, got {t.dtype} on {t.device}")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{what}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    raise ValueError(f"{what} must be contiguous")
+_calls_module = None
 
 
-def _arg(t, what, dtype, dev, shape=None):
-    """Address of a dense tensor argument of the given element type, device and shape; None stays None."""
-    if t is None:
-        return None
-    if t.dtype is not dtype or t.device != dev or (shape is not None and t.shape != shape) or not t.is_contiguous():
-        _refuse(t, what, dtype, dev, shape)
-    return t.data_ptr()
+def _calls():
+    """The module of these calls on torch tensors (csrc/torch_calls.cpp): checks of element types, devices,
+    shapes and layouts (ValueError), outputs and workspace from torch, and the entry point on the tensors'
+    device and that device's current stream, in C++, because a decoding step makes them for every layer."""
+    global _calls_module
+    if _calls_module is None:
+        lib = load()
+        try:
+            from . import _torch_calls as m
+        except ImportError as e:
+            raise ImportError("_torch_calls.so not found or not loadable: build it with "
+                              "`python -m gated_delta_rule_107_b200.build`") from e
+        m.bind(*(ctypes.cast(getattr(lib, "delta_rule_" + f), ctypes.c_void_p).value for f in (
+            "pages", "qkrope", "qkrope_workspace_size", "qkrope_bwd", "qkrope_cache", "attn_decode_workspace_size",
+            "attn_decode")))
+        _calls_module = m
+    return _calls_module
 
 
-def _token_stride(t, what, dtype, dev):
-    """Elements from a token to the next of a [B, T, H, d] or [N, H, d] tensor with dense heads."""
-    if t.dtype is not dtype or t.device != dev:
-        _refuse(t, what, dtype, dev, None)
-    shape, st = t.shape, t.stride()
-    ok = len(shape) in (3, 4)
-    if ok:
-        H, d, tok = shape[-2], shape[-1], st[-3]
-        ok = st[-1] == 1 and (st[-2] == d or H == 1)
-        if len(shape) == 4 and shape[1] == 1:
-            tok = st[0]
-        elif len(shape) == 4 and shape[0] > 1:
-            ok = ok and st[0] == shape[1] * tok
-        if shape[-3] == 1 and (len(shape) == 3 or shape[0] == 1):
-            tok = H * d  # one token: its stride says nothing
-    if not ok:
-        raise ValueError(f"{what}: expected [B, T, H, d] or [N, H, d] with dense heads and evenly spaced tokens, "
-                         f"got strides {st} of shape {tuple(shape)}")
-    return tok
-
-
-def _cuda(t, what):
-    dev = t.device
-    if dev.type != "cuda":
-        raise ValueError(f"{what} must be a CUDA tensor")
-    if t.dtype not in DTYPES:
-        raise ValueError(f"{what}: expected torch.float32 or torch.bfloat16, got {t.dtype}")
-    return dev
-
-
-# The current stream's handle.  torch.cuda.current_stream() builds a Stream object first, which takes
-# about as long (3 us) as the rest of a small call's arguments together.
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
-    lambda index: torch.cuda.current_stream(index).cuda_stream)
-
-
-def _launch(fn, what, dev, *args):
-    """Calls a C entry point on the tensors' device and that device's current stream (the last argument)."""
-    index = dev.index
-    if torch.cuda.current_device() == index:
-        rc = fn(*args, _raw_stream(index))
-    else:
-        with torch.cuda.device(dev):
-            rc = fn(*args, _raw_stream(index))
-    if rc != DR_OK:
-        raise DeltaRuleError(rc, what)
-
-
-def _dense_like(t):
-    return torch.empty_like(t, memory_format=torch.contiguous_format)
+def _given(r, what):
+    """The tensors of a call of _calls(), which returns the entry point's error code instead when it refuses."""
+    if type(r) is int:
+        raise DeltaRuleError(r, what)
+    return r
 
 
 def delta_rule_pages(cached, fresh, free_pages, n_free, table, page, tokens):
@@ -686,44 +646,7 @@ def delta_rule_pages(cached, fresh, free_pages, n_free, table, page, tokens):
     free pages, and n_free: int32 [1], how many of it are free; table: int32 [R, width], the block table,
     whose new entries are written in place; page: tokens a page holds; tokens: the rows of the step's
     (padded) batch.  All stay on the GPU; the next step passes n_left as its n_free."""
-    dev = cached.device
-    if dev.type != "cuda":
-        raise ValueError("cached must be a CUDA tensor")
-    i32 = torch.int32
-    if cached.dim() != 1 or table.dim() != 2 or free_pages.dim() != 1 or n_free.numel() != 1:
-        raise ValueError("delta_rule_pages takes cached, fresh [R], free_pages [F], n_free [1], table [R, width]")
-    R, tokens = cached.shape[0], int(tokens)
-    if table.shape[0] != R or tokens < 0:
-        raise ValueError(f"table: expected {R} rows, got {table.shape[0]} (tokens {tokens})")
-    ints = torch.empty(2 * R + 2 + tokens, dtype=i32, device=dev)
-    lens, cu_new, n_left, positions = ints.split((R, R + 1, 1, tokens))
-    slots = torch.empty(tokens, dtype=torch.int64, device=dev)
-    at = ints.data_ptr()
-    _launch(load().delta_rule_pages, "delta_rule_pages", dev, _arg(cached, "cached", i32, dev),
-            _arg(fresh, "fresh", i32, dev, cached.shape), _arg(free_pages, "free_pages", i32, dev),
-            _arg(n_free, "n_free", i32, dev), _arg(table, "table", i32, dev), at, at + 4 * R, at + 8 * R + 8,
-            slots.data_ptr(), at + 8 * R + 4, R, free_pages.shape[0], table.shape[1], int(page), tokens)
-    return lens, cu_new, positions, slots, n_left
-
-
-def _qk(q, k, wq, wk, inv_freq, positions):
-    """What the forms of the norm with rotation check alike."""
-    dev, dt = _cuda(q, "q"), q.dtype
-    qs, ks = _token_stride(q, "q", dt, dev), _token_stride(k, "k", dt, dev)
-    d = q.shape[-1]
-    if k.shape[:-2] != q.shape[:-2] or k.shape[-1] != d:
-        raise ValueError(f"k: expected the tokens and channels of q {tuple(q.shape)}, got {tuple(k.shape)}")
-    if q.dim() == 4:
-        B, T = q.shape[0], q.shape[1]
-    else:
-        B, T = 1, q.shape[0]
-    rot = 0 if inv_freq is None else 2 * inv_freq.numel()
-    w = (d,)
-    if positions is not None and positions.numel() != B * T:
-        raise ValueError(f"positions: expected one for each of {B * T} tokens, got {positions.numel()}")
-    return (dev, dt, B, T, d, rot, qs, ks, _arg(wq, "wq", torch.float32, dev, w),
-            _arg(wk, "wk", torch.float32, dev, w), _arg(inv_freq, "inv_freq", torch.float64, dev),
-            _arg(positions, "positions", torch.int32, dev))
+    return _given(_calls().pages(cached, fresh, free_pages, n_free, table, page, tokens), "delta_rule_pages")
 
 
 def delta_rule_qkrope(q, k, wq=None, wk=None, inv_freq=None, positions=None, interleaved=False):
@@ -732,86 +655,23 @@ def delta_rule_qkrope(q, k, wq=None, wk=None, inv_freq=None, positions=None, int
     q [B, T, Hq, d], k [B, T, Hk, d] (or [N, H, d]; slices of one projection are read in place); wq, wk
     fp32 [d] or None; inv_freq fp64 [rot / 2] or None (no rotation); positions int32 [B, T] or None
     (0 .. T - 1); interleaved: channel pairs (2i, 2i + 1) instead of (i, i + rot / 2)."""
-    dev, dt, B, T, d, rot, qs, ks, wqp, wkp, fp, pp_ = _qk(q, k, wq, wk, inv_freq, positions)
-    q_out, k_out = _dense_like(q), _dense_like(k)
-    _launch(load().delta_rule_qkrope, "delta_rule_qkrope", dev, q.data_ptr(), k.data_ptr(), wqp, wkp, fp, pp_,
-            q_out.data_ptr(), k_out.data_ptr(), B, T, q.shape[-2], k.shape[-2], d, rot, int(interleaved), qs, ks,
-            DTYPES[dt])
-    return q_out, k_out
-
-
-@functools.lru_cache(maxsize=None)
-def qkrope_workspace_size(d) -> int:
-    n = load().delta_rule_qkrope_workspace_size(d)
-    if n == ctypes.c_size_t(-1).value:
-        raise DeltaRuleError(DR_ERR_UNSUPPORTED, "delta_rule_qkrope_workspace_size")
-    return n
+    return _given(_calls().qkrope(q, k, wq, wk, inv_freq, positions, interleaved), "delta_rule_qkrope")
 
 
 def delta_rule_qkrope_bwd(q, k, wq, wk, inv_freq, dq_out, dk_out, positions=None, interleaved=False, dq=None,
                           dk=None, want_dw=True):
     """Gradients (dq, dk, dwq, dwk) of delta_rule_qkrope for dq_out, dk_out (dense); dwq, dwk fp32 [d]
     (None without want_dw).  dq, dk may be given: slices of one projection's gradient, say."""
-    dev, dt, B, T, d, rot, qs, ks, wqp, wkp, fp, pp_ = _qk(q, k, wq, wk, inv_freq, positions)
-    if dq is None:
-        dq = _dense_like(q)
-    if dk is None:
-        dk = _dense_like(k)
-    if dq.shape != q.shape or dk.shape != k.shape:
-        raise ValueError("dq, dk must be shaped like q, k")
-    dqs, dks = _token_stride(dq, "dq", dt, dev), _token_stride(dk, "dk", dt, dev)
-    dwq = dwk = None
-    if want_dw:
-        dwq, dwk = (torch.empty(d, dtype=torch.float32, device=dev) if w is None else torch.empty_like(w)
-                    for w in (wq, wk))
-    need = qkrope_workspace_size(d) if want_dw else 0
-    ws = torch.empty(need, dtype=torch.uint8, device=dev) if want_dw else None
-    _launch(load().delta_rule_qkrope_bwd, "delta_rule_qkrope_bwd", dev, q.data_ptr(), k.data_ptr(), wqp, wkp, fp, pp_,
-            _arg(dq_out, "dq_out", dt, dev, q.shape), _arg(dk_out, "dk_out", dt, dev, k.shape), dq.data_ptr(),
-            dk.data_ptr(), dwq.data_ptr() if want_dw else None, dwk.data_ptr() if want_dw else None, B, T, q.shape[-2], k.shape[-2], d, rot,
-            int(interleaved), qs, ks, dqs, dks, DTYPES[dt], None if ws is None else ws.data_ptr(), need)
-    return dq, dk, dwq, dwk
-
-
-def _page_stride(t, what, dtype, dev):
-    """Elements from a page to the next of a cache [pages, page, Hk, d], dense inside a page."""
-    if t.dtype != dtype or t.device != dev or t.dim() != 4:
-        raise ValueError(f"{what}: expected a {dtype} [pages, page, Hk, d] on {dev}, got {t.dtype} "
-                         f"{tuple(t.shape)} on {t.device}")
-    n, page, H, d = t.shape
-    st = t.stride()
-    if st[3] != 1 or (H > 1 and st[2] != d) or (page > 1 and st[1] != H * d):
-        raise ValueError(f"{what} must be dense inside a page, got strides {st}")
-    return st[0] if n > 1 else max(st[0], page * H * d)
+    return _given(_calls().qkrope_bwd(q, k, wq, wk, inv_freq, positions, interleaved, dq_out, dk_out, dq, dk,
+                                      want_dw), "delta_rule_qkrope_bwd")
 
 
 def delta_rule_qkrope_cache(q, k, v, wq, wk, inv_freq, positions, slots, k_cache, v_cache, interleaved=False,
                             q_out=None):
     """delta_rule_qkrope for serving: returns q_out; the keys (normed, rotated) and the values go into rows
     slots (int64, one a token; negative: padding, not written) of the caches [pages, page, Hk, d]."""
-    dev, dt, B, T, d, rot, qs, ks, wqp, wkp, fp, pp_ = _qk(q, k, wq, wk, inv_freq, positions)
-    vs = _token_stride(v, "v", dt, dev)
-    if v.shape != k.shape or positions is None or slots.numel() != B * T:
-        raise ValueError("delta_rule_qkrope_cache takes v shaped like k, and a position and a slot for each token")
-    kps, vps = _page_stride(k_cache, "k_cache", dt, dev), _page_stride(v_cache, "v_cache", dt, dev)
-    if k_cache.shape != v_cache.shape or k_cache.shape[2:] != k.shape[-2:]:
-        raise ValueError(f"the caches must be [pages, page, {k.shape[-2]}, {d}], got {tuple(k_cache.shape)}, "
-                         f"{tuple(v_cache.shape)}")
-    if q_out is None:
-        q_out = _dense_like(q)
-    _launch(load().delta_rule_qkrope_cache, "delta_rule_qkrope_cache", dev, q.data_ptr(), k.data_ptr(), v.data_ptr(),
-            wqp, wkp, fp, pp_, _arg(slots, "slots", torch.int64, dev), _arg(q_out, "q_out", dt, dev, q.shape),
-            k_cache.data_ptr(), v_cache.data_ptr(), B * T, q.shape[-2], k.shape[-2], d, rot, int(interleaved), qs, ks,
-            vs, k_cache.shape[0], k_cache.shape[1], kps, vps, DTYPES[dt])
-    return q_out
-
-
-@functools.lru_cache(maxsize=None)
-def attn_decode_workspace_size(Hq, Hk, d, dtype) -> int:
-    n = load().delta_rule_attn_decode_workspace_size(Hq, Hk, d, dtype)
-    if n == ctypes.c_size_t(-1).value:
-        raise DeltaRuleError(DR_ERR_ARG, "delta_rule_attn_decode_workspace_size")
-    return n
+    return _given(_calls().qkrope_cache(q, k, wq, wk, inv_freq, positions, interleaved, v, slots, k_cache, v_cache,
+                                        q_out), "delta_rule_qkrope_cache")[0]
 
 
 def delta_rule_attn_decode(q, k_cache, v_cache, table, lens, scale=None, window=0, want_lse=False, out=None,
@@ -820,29 +680,8 @@ def delta_rule_attn_decode(q, k_cache, v_cache, table, lens, scale=None, window=
 
     q [R, Hq, d]; caches [pages, page, Hk, d]; table int32 [R, width]; lens int32 [R], cached tokens, the
     new one among them; scale: of the scores (None: d ** -0.5); window: the last tokens seen (0: all)."""
-    dev, dt = _cuda(q, "q"), q.dtype
-    if q.dim() != 3 or table.dim() != 2:
-        raise ValueError("delta_rule_attn_decode takes q [R, Hq, d] and table [R, width]")
-    R, Hq, d = q.shape
-    kps, vps = _page_stride(k_cache, "k_cache", dt, dev), _page_stride(v_cache, "v_cache", dt, dev)
-    n_pages, page, Hk, dk = k_cache.shape
-    if k_cache.shape != v_cache.shape or dk != d:
-        raise ValueError(f"the caches must be [pages, page, Hk, {d}], got {tuple(k_cache.shape)}, "
-                         f"{tuple(v_cache.shape)}")
-    if table.shape[0] != R:
-        raise ValueError(f"table: expected {R} rows, got {table.shape[0]}")
-    if out is None:
-        out = _dense_like(q)
-    lse = torch.empty((R, Hq), dtype=torch.float32, device=dev) if want_lse else None
-    need = attn_decode_workspace_size(Hq, Hk, d, DTYPES[dt])
-    if workspace is None or workspace.numel() < need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    _launch(load().delta_rule_attn_decode, "delta_rule_attn_decode", dev, _arg(q, "q", dt, dev), k_cache.data_ptr(),
-            v_cache.data_ptr(), _arg(table, "table", torch.int32, dev), _arg(lens, "lens", torch.int32, dev, (R,)),
-            _arg(out, "out", dt, dev, q.shape), None if lse is None else lse.data_ptr(), R, Hq, Hk, d, n_pages, page,
-            table.shape[1], kps, vps, d ** -0.5 if scale is None else float(scale), int(window), DTYPES[dt],
-            _arg(workspace, "workspace", torch.uint8, dev), need)
-    return out, lse
+    return _given(_calls().attn_decode(q, k_cache, v_cache, table, lens, scale, window, want_lse, out, workspace),
+                  "delta_rule_attn_decode")
 
 
 def delta_rule_fwd_host(q, k, v, alpha, beta, S0=None, variant="gdn", chunk=64, device="cuda"):

@@ -1,4 +1,4 @@
-"""Build libdeltarule.so in-tree with nvcc for sm_100a."""
+"""Build libdeltarule.so in-tree with nvcc for sm_100a, and the host module of calls on torch tensors."""
 from __future__ import annotations
 
 import glob
@@ -8,6 +8,8 @@ import subprocess
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libdeltarule.so")
+CALLS = os.path.join(HERE, "_torch_calls.so")
+CALLS_SRC = [os.path.join(CSRC, "torch_calls.cpp"), os.path.join(os.path.dirname(HERE), "include", "delta_rule.h")]
 ROOT = os.path.dirname(HERE)
 
 NVCC_FLAGS = [
@@ -44,8 +46,32 @@ KERNEL_FILES = {
 }
 
 
+def build_calls(force: bool = False, verbose: bool = False) -> str:
+    """Compile csrc/torch_calls.cpp (host code against torch's and Python's headers) into _torch_calls.so."""
+    newest = max(os.path.getmtime(p) for p in CALLS_SRC)
+    if not force and os.path.exists(CALLS) and os.path.getmtime(CALLS) >= newest:
+        return CALLS
+    import sysconfig
+
+    import torch
+    t = os.path.join(os.path.dirname(torch.__file__))
+    cuda = os.path.join(os.environ.get("CUDA_HOME", "/usr/local/cuda"), "include")
+    tmp = CALLS + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-o", tmp, CALLS_SRC[0],
+           "-isystem", os.path.join(t, "include"), "-isystem", os.path.join(t, "include", "torch", "csrc", "api", "include"),
+           "-isystem", sysconfig.get_paths()["include"], "-isystem", cuda, "-L" + os.path.join(t, "lib"),
+           "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch", "-ltorch_python"]
+    if verbose:
+        print(" ".join(cmd))
+    subprocess.check_call(cmd)
+    os.replace(tmp, CALLS)
+    return CALLS
+
+
 def build(force: bool = False, verbose: bool = False, extra: list[str] | None = None) -> str:
-    """Compile csrc/delta_rule_lib.cu (the unity translation unit) into libdeltarule.so."""
+    """Compile csrc/delta_rule_lib.cu (the unity translation unit) into libdeltarule.so, and csrc/torch_calls.cpp."""
+    build_calls(force, verbose)
     newest = max(os.path.getmtime(p) for p in sources())
     if not force and os.path.exists(LIB) and os.path.getmtime(LIB) >= newest:
         return LIB

@@ -197,17 +197,21 @@ def test_python_level_refusals():
         b.delta_rule_attn_decode(x, x, x, x, x)
     with pytest.raises(ValueError):
         b.delta_rule_pages(x, x, x, x, x, 16, 4)
-    dev = x.device
-    assert b._token_stride(torch.zeros(5, 6 * 64).unflatten(-1, (6, 64))[:, 2:4], "q", torch.float32, dev) == 384
-    assert b._token_stride(torch.zeros(2, 5, 6, 64)[:, :, 1:3], "q", torch.float32, dev) == 384
-    assert b._token_stride(torch.zeros(2, 5, 6, 64)[:, :1], "q", torch.float32, dev) == 5 * 384
-    assert b._token_stride(torch.zeros(1, 1, 6, 64), "q", torch.float32, dev) == 384
+    tok, pg = b._calls().stride_of_tokens, b._calls().stride_of_pages
+    assert tok(torch.zeros(5, 6 * 64).unflatten(-1, (6, 64))[:, 2:4]) == 384
+    assert tok(torch.zeros(2, 5, 6, 64)[:, :, 1:3]) == 384
+    assert tok(torch.zeros(2, 5, 6, 64)[:, :1]) == 5 * 384
+    assert tok(torch.zeros(1, 1, 6, 64)) == tok(torch.zeros(3, 6, 64)[1:2]) == tok(torch.zeros(1, 7, 64)[:, :6]) == 384
     for bad in (torch.zeros(2, 5, 6, 64)[:, :3], torch.zeros(5, 64, 6).transpose(1, 2), torch.zeros(5, 6, 128)[..., ::2],
                 torch.zeros(6, 64), torch.zeros(5, 6, 128)[..., :64]):
         with pytest.raises(ValueError):
-            b._token_stride(bad, "q", torch.float32, dev)
-    assert b._page_stride(torch.zeros(4, 2, 16, 2, 64)[:, 1], "kc", torch.float32, dev) == 2 * 16 * 2 * 64
-    assert b._page_stride(torch.zeros(1, 2, 16, 2, 64)[:, 1], "kc", torch.float32, dev) >= 16 * 2 * 64
+            tok(bad)
+    assert pg(torch.zeros(4, 2, 16, 2, 64)[:, 1]) == 2 * 16 * 2 * 64
+    assert pg(torch.zeros(1, 2, 16, 2, 64)[:, 1]) == 16 * 2 * 64
     for bad in (torch.zeros(4, 16, 4, 64)[:, :, 1:3], torch.zeros(4, 2, 16, 64).transpose(1, 2), torch.zeros(4, 16, 64)):
         with pytest.raises(ValueError):
-            b._page_stride(bad, "kc", torch.float32, dev)
+            pg(bad)
+    with pytest.raises(TypeError):
+        tok(3)
+    with pytest.raises(TypeError):
+        b.delta_rule_qkrope(None, x)
