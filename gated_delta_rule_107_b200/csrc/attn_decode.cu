@@ -523,7 +523,8 @@ template <class C, int D> __global__ void __launch_bounds__(THREADS) k_attn(cons
     const AttnDecode &a = x.a;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int segs = a.Hk * x.RB;
-    asm volatile("griddepcontrol.launch_dependents;");  // the join may take its places; it waits for this kernel's end
+    let_next();  // k_attn_join: small blocks, wanted at once
+    after_previous();
     const Run run = find_run(x, segs);
     for (int r = blockIdx.x; r < a.R; r += gridDim.x) {  // requests that see nothing
         Span sp;
@@ -659,7 +660,7 @@ template <class C, int D> __global__ void __launch_bounds__(THREADS) k_attn(cons
 // The split segment that begins in run blockIdx.x: one head (blockIdx.y), its parts added in order.
 template <typename E, int D> __global__ void __launch_bounds__(256) k_attn_join(const Args x) {
     __shared__ float red[8][D], wm[8], wl[8];
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    after_previous();
     const int4 hd = x.head[blockIdx.x];
     if (hd.x < 0) return;
     const int rb = hd.z & 0xffff, slot0 = hd.z >> 16, GB = x.GB, in = blockIdx.y, head = hd.y * x.G + rb * GB + in;
@@ -699,6 +700,7 @@ template <typename E, int D> __global__ void __launch_bounds__(256) k_attn_join(
         ((E *)x.a.out)[row * D + c] = from_f<E>(l > 0.f ? s / l : (l == l ? 0.f : l));
     }
     if (threadIdx.x == 0 && x.a.lse) x.a.lse[row] = lse_of(m, l);
+    let_next();
 }
 
 template <class C, int D> static cudaError_t launch(Args x, cudaStream_t s) {
@@ -714,11 +716,9 @@ template <class C, int D> static cudaError_t launch(Args x, cudaStream_t s) {
     // no more CTAs than the tables have room for runs
     const double tiles = (double)a.R * a.Hk * x.RB * ((double)a.width * a.page / TILE + 1 + COST);
     const int ctas = tiles / MIN_UNITS < C::CTAS - 1 ? (int)(tiles / MIN_UNITS) + 1 : C::CTAS;
-    k_attn<C, D><<<ctas, THREADS, smem, s>>>(x);
-    e = cudaGetLastError();
+    e = launch_after(k_attn<C, D>, dim3(ctas), dim3(THREADS), smem, s, x);
     if (e != cudaSuccess) return e;
-    // set up while k_attn runs, so that only its work follows (2 us less on the smallest calls)
-    return launch_after(k_attn_join<typename C::E, D>, dim3(ctas, x.G < C::GB ? x.G : C::GB), dim3(256), s, x);
+    return launch_after(k_attn_join<typename C::E, D>, dim3(ctas, x.G < C::GB ? x.G : C::GB), dim3(256), 0, s, x);
 }
 
 static int heads_per_block(int G, bool bf16) {

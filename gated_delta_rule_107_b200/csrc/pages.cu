@@ -49,6 +49,7 @@ template <int UNROLL> __global__ void __launch_bounds__(MAX_THREADS) k_pages(con
     __shared__ int wsum[2][MAX_THREADS / 32];
     const int threads = blockDim.x;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    after_previous();
     // each thread sums a run of requests, then the runs are scanned over the CTA
     const int per = (p.R + threads - 1) / threads, r0 = min(p.R, tid * per), r1 = min(p.R, r0 + per);
     int sc = 0, st = 0;
@@ -76,10 +77,15 @@ template <int UNROLL> __global__ void __launch_bounds__(MAX_THREADS) k_pages(con
     int ec = __shfl_up_sync(0xffffffffu, ic, 1), et = __shfl_up_sync(0xffffffffu, it, 1);
     if (lane == 0) ec = et = 0;
     __syncthreads();
-    for (int w = 0; w < warp; ++w) {
-        ec = add_sat(ec, wsum[0][w]);
-        et = add_sat(et, wsum[1][w]);
+    // the sums of the warps before, by shuffles (saturated sums may be added in any order)
+    int bc = lane < warp ? wsum[0][lane] : 0, bt = lane < warp ? wsum[1][lane] : 0;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        bc = add_sat(bc, __shfl_xor_sync(0xffffffffu, bc, o));
+        bt = add_sat(bt, __shfl_xor_sync(0xffffffffu, bt, o));
     }
+    ec = add_sat(ec, bc);
+    et = add_sat(et, bt);
     for (int r = r0; r < r1; ++r) {
         const int xc = c[r], xt = t[r];
         c[r] = ec;
@@ -135,6 +141,7 @@ template <int UNROLL> __global__ void __launch_bounds__(MAX_THREADS) k_pages(con
             p.slots[n] = pg[k] < 0 ? -1ll : (long long)pg[k] * p.page + (pos[k] - p.by_page.div(pos[k]) * p.page);
         }
     }
+    let_next();
 }
 
 }  // namespace pgs
@@ -144,9 +151,9 @@ cudaError_t pages_run(const Pages &args, cudaStream_t s) {
     p.by_page = FastDiv(p.page);
     const size_t smem = 2 * ((size_t)p.R + 1) * sizeof(int);
     // One token a lane in CTAs of 256 threads while one wave of them holds all tokens (66 tokens of 64
-    // requests: 3.3 us, four a lane 5.1), else four a lane, whose reads overlap and whose search is
+    // requests: 3.6 us, four a lane 5.1), else eight a lane, whose reads overlap and whose search is
     // shared, in CTAs of 1024, so that the prefix sums are formed once an SM (10^6 tokens of 509
-    // requests: 10.1 us, one a lane 15.3).  The requests' own outputs need a thread each as well.
+    // requests: 8.2 us, four a lane 9.4, one a lane 15.3).  The requests' own outputs need a thread each as well.
     const long long most = p.N > p.R ? p.N : p.R;
     auto go = [&](auto kern, int threads, int unroll) -> cudaError_t {
         if (smem > 48 * 1024) {
@@ -155,10 +162,9 @@ cudaError_t pages_run(const Pages &args, cudaStream_t s) {
         }
         long long ctas = (most + threads * unroll - 1) / (threads * unroll);
         ctas = ctas < 1 ? 1 : (ctas > pgs::MAX_CTAS ? pgs::MAX_CTAS : ctas);
-        kern<<<(unsigned)ctas, threads, smem, s>>>(p);
-        return cudaGetLastError();
+        return launch_after(kern, dim3((unsigned)ctas), dim3(threads), smem, s, p);
     };
-    return most <= 256 * pgs::MAX_CTAS ? go(pgs::k_pages<1>, 256, 1) : go(pgs::k_pages<4>, pgs::MAX_THREADS, 4);
+    return most <= 256 * pgs::MAX_CTAS ? go(pgs::k_pages<1>, 256, 1) : go(pgs::k_pages<8>, pgs::MAX_THREADS, 8);
 }
 
 }  // namespace dr

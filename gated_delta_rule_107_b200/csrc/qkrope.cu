@@ -263,6 +263,7 @@ __global__ void __launch_bounds__(THREADS, 3) k_qkrope(const QkRope p, int hpg) 
     const unsigned N = (unsigned)p.N, step = gridDim.x * (THREADS / 32) * TPW;  // N < 2^31: no sum wraps
     unsigned n0 = (blockIdx.x * (THREADS / 32) + (threadIdx.x >> 5)) * TPW;
 
+    after_previous();
     Ring<2, PF_FWD> ring(ring_smem);
     auto token = [&](unsigned at) { return (size_t)min(at + lane / LPT, N - 1); };  // behind the last: computed, not stored
     unsigned ln = n0;               // the token whose row is copied next,
@@ -363,6 +364,7 @@ __global__ void __launch_bounds__(THREADS, 3) k_qkrope(const QkRope p, int hpg) 
             }
         }
     }
+    let_next();
 }
 
 // The rows of TPW tokens side by side are a warp's item: TPW tokens x one head.  The items, head by head and then on to the next tokens, are one list cut
@@ -391,7 +393,8 @@ __global__ void __launch_bounds__(THREADS, 2) k_qkrope_bwd(const QkRope p, long 
     const L l(j, p.rot);
     Items<TPW> now(p, p.Hq + p.Hk, per);
 
-    asm volatile("griddepcontrol.launch_dependents;");
+    if (p.part) let_next();  // k_qkrope_dw: few blocks, wanted at once
+    after_previous();
     Ring<4, PF_BWD> ring(ring_smem);
     const unsigned N = (unsigned)p.N;
     auto token = [&](unsigned at) { return (size_t)min(at + lane / LPT, N - 1); };
@@ -518,7 +521,7 @@ __global__ void __launch_bounds__(THREADS, 2) k_qkrope_bwd(const QkRope p, long 
 // dwq, dwk = the partials' sums in order: 32 columns a CTA, 32 partials at a time
 template <int D> __global__ void __launch_bounds__(1024) k_qkrope_dw(const float *part, int n, float *dwq, float *dwk) {
     __shared__ float red[32][33];
-    asm volatile("griddepcontrol.wait;" ::: "memory");  // launched while the partials are being formed
+    after_previous();
     const int cx = threadIdx.x & 31, ry = threadIdx.x >> 5, col = blockIdx.x * 32 + cx;
     float s = 0.f;
     for (int r = ry; r < n; r += 32) s += part[(size_t)r * 2 * D + col];
@@ -533,6 +536,7 @@ template <int D> __global__ void __launch_bounds__(1024) k_qkrope_dw(const float
             dwk[at - D] = s;
         }
     }
+    let_next();
 }
 
 template <typename E, int D, bool INTER> static cudaError_t fwd(const QkRope &p, cudaStream_t s) {
@@ -549,8 +553,7 @@ template <typename E, int D, bool INTER> static cudaError_t fwd(const QkRope &p,
         constexpr int smem = Ring<2, PF_FWD>::WARP_BYTES * (THREADS / 32);
         const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
-        kern<<<grid, THREADS, smem, s>>>(p, hpg);
-        return cudaGetLastError();
+        return launch_after(kern, grid, dim3(THREADS), smem, s, p, hpg);
     };
     return cache ? go(k_qkrope<E, D, INTER, true>) : go(k_qkrope<E, D, INTER, false>);
 }
@@ -562,14 +565,13 @@ template <typename E, int D, bool INTER> static cudaError_t bwd(const QkRope &p,
     const long long items = (long long)((p.N + TPW - 1) / TPW) * (p.Hq + p.Hk), per = (items + WARPS - 1) / WARPS;
     const int ctas = (int)((items + per * (THREADS / 32) - 1) / (per * (THREADS / 32)));
     constexpr int smem = Ring<4, PF_BWD>::WARP_BYTES * (THREADS / 32);
-    const cudaError_t e = cudaFuncSetAttribute(k_qkrope_bwd<E, D, INTER>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    cudaError_t e = cudaFuncSetAttribute(k_qkrope_bwd<E, D, INTER>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     QkRope a = p;
     if (!p.dwq && !p.dwk) a.part = nullptr;
-    k_qkrope_bwd<E, D, INTER><<<ctas, THREADS, smem, s>>>(a, per);
-    const cudaError_t e2 = cudaGetLastError();
-    if (e2 != cudaSuccess || !a.part) return e2;
-    return launch_after(k_qkrope_dw<D>, dim3(2 * D / 32), dim3(1024), s, (const float *)a.part, ctas, p.dwq, p.dwk);
+    e = launch_after(k_qkrope_bwd<E, D, INTER>, dim3(ctas), dim3(THREADS), smem, s, a, per);
+    if (e != cudaSuccess || !a.part) return e;
+    return launch_after(k_qkrope_dw<D>, dim3(2 * D / 32), dim3(1024), 0, s, (const float *)a.part, ctas, p.dwq, p.dwk);
 }
 
 template <typename F> static cudaError_t by_type(const QkRope &p, bool bf16, F f) {
