@@ -61,7 +61,9 @@ def build_calls(force: bool = False, verbose: bool = False) -> str:
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-o", tmp, CALLS_SRC[0],
            "-isystem", os.path.join(t, "include"), "-isystem", os.path.join(t, "include", "torch", "csrc", "api", "include"),
            "-isystem", sysconfig.get_paths()["include"], "-isystem", cuda, "-L" + os.path.join(t, "lib"),
-           "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch", "-ltorch_python"]
+           "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch", "-ltorch_python",
+           # torch's own C++ runtime: a second, static one would not know torch's exceptions
+           "-nostdlib++", "-l:libstdc++.so.6"]
     if verbose:
         print(" ".join(cmd))
     subprocess.check_call(cmd)

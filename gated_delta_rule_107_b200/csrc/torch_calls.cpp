@@ -9,6 +9,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -120,7 +121,11 @@ struct On {
     explicit On(at::Device dev) : guard(dev), stream(c10::cuda::getCurrentCUDAStream(dev.index()).stream()) {}
 };
 
-at::Tensor like(const at::Tensor &t) { return at::empty(t.sizes(), t.options()); }
+// a new dense tensor, straight from the allocator (at::empty's dispatch takes as long again)
+at::Tensor empty(at::IntArrayRef shape, at::ScalarType type, at::Device dev) {
+    return at::detail::empty_cuda(shape, type, dev, std::nullopt);
+}
+at::Tensor like(const at::Tensor &t) { return empty(t.sizes(), t.scalar_type(), t.device()); }
 
 PyObject *code(int rc) { return PyLong_FromLong(rc); }
 template <typename... T> PyObject *give(const T &...t) {
@@ -156,9 +161,8 @@ PyObject *pages(PyObject *, Args a, Py_ssize_t n) {
          *sp = dense(stack, "free_pages", at::kInt, dev, -1), *np = dense(n_free, "n_free", at::kInt, dev, 1),
          *tp = dense(table, "table", at::kInt, dev, -1);
     On on(dev);
-    const auto opt = cached.options();
-    at::Tensor lens = at::empty({R}, opt), cu = at::empty({R + 1}, opt), pos = at::empty({N}, opt), left = at::empty({1}, opt),
-               slots = at::empty({N}, opt.dtype(at::kLong));
+    at::Tensor lens = empty({R}, at::kInt, dev), cu = empty({R + 1}, at::kInt, dev), pos = empty({N}, at::kInt, dev),
+               left = empty({1}, at::kInt, dev), slots = empty({N}, at::kLong, dev);
     const int rc = c_pages((int *)cp, (int *)fp, (int *)sp, (int *)np, (int *)tp, (int *)lens.data_ptr(), (int *)cu.data_ptr(),
                            (int *)pos.data_ptr(), (long long *)slots.data_ptr(), (int *)left.data_ptr(), R,
                            extent(stack.numel(), "free_pages"), extent(table.size(1), "table"), page, N, on.stream);
@@ -238,10 +242,9 @@ PyObject *qkrope_bwd(PyObject *, Args a, Py_ssize_t n) {
     if (want) {
         need = c_qkrope_ws(x.d);
         if (need == (size_t)-1) return code(DR_ERR_UNSUPPORTED);
-        const auto opt = x.q.options();
-        dwq = at::empty({x.d}, opt.dtype(at::kFloat));
-        dwk = at::empty({x.d}, opt.dtype(at::kFloat));
-        ws = at::empty({(int64_t)need}, opt.dtype(at::kByte));
+        dwq = empty({x.d}, at::kFloat, x.dev);
+        dwk = empty({x.d}, at::kFloat, x.dev);
+        ws = empty({(int64_t)need}, at::kByte, x.dev);
     }
     const int rc = c_qkrope_bwd(x.q.data_ptr(), x.k.data_ptr(), x.wq, x.wk, x.f, x.pos, gqp, gkp, dq.data_ptr(), dk.data_ptr(),
                                 want ? (float *)dwq.data_ptr() : nullptr, want ? (float *)dwk.data_ptr() : nullptr, x.B, x.T,
@@ -314,12 +317,12 @@ PyObject *attn_decode(PyObject *, Args a, Py_ssize_t n) {
     const at::Tensor out = out_like(a[8], "out", q);
     TORCH_CHECK_VALUE(out.is_contiguous(), "out must be contiguous");
     at::Tensor lse, ws;
-    if (want) lse = at::empty({R, Hq}, q.options().dtype(at::kFloat));
+    if (want) lse = empty({R, Hq}, at::kFloat, dev);
     if (a[9] != Py_None) {
         ws = tensor(a[9], "workspace");
         dense(ws, "workspace", at::kByte, dev, -1);
     }
-    if (!ws.defined() || (size_t)ws.numel() < need) ws = at::empty({(int64_t)need}, q.options().dtype(at::kByte));
+    if (!ws.defined() || (size_t)ws.numel() < need) ws = empty({(int64_t)need}, at::kByte, dev);
     const int rc = c_attn(qp, kc.data_ptr(), vc.data_ptr(), (int *)tp, (int *)lp, out.data_ptr(),
                           want ? (float *)lse.data_ptr() : nullptr, R, Hq, Hk, d, extent(kc.size(0), "k_cache"),
                           extent(kc.size(1), "k_cache"), extent(table.size(1), "table"), kps, vps, (float)scale, window, dtype,
