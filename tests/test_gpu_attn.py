@@ -493,6 +493,102 @@ def test_attn_decode_streams_and_graphs():
         _check_attn(o, lse, q, kc, vc, table, new, "bf16", what=f"replayed {new}")
 
 
+def test_attn_decode_behind_copies_in_a_graph():
+    """Copies and other libraries' kernels between the calls, eager and captured: every call sees what was
+    enqueued before it, although its kernels are set up while those still run."""
+    lens = [4000, 1, 900]
+    kc, vc, table = _cache("bf16", lens, 16, 1, 128, seed=23)
+    q1, q2 = _randn(_rng(1), 3, 4, 128, dtype="bf16"), _randn(_rng(2), 3, 4, 128, dtype="bf16")
+    ln = _i32(lens)
+    want = [binding.delta_rule_attn_decode(x, kc, vc, table, ln)[0].clone() for x in (q1, q2)]
+    q, n = torch.zeros_like(q1), torch.zeros_like(ln)
+
+    def step(src):
+        n.zero_()
+        q.fill_(7.0)
+        q.copy_(src)                               # a copy node
+        n.copy_(ln)
+        o, _ = binding.delta_rule_attn_decode(q, kc, vc, table, n)
+        return o * 1.0                             # another kernel behind it
+
+    for _ in range(20):
+        got = [step(q1), step(q2)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = [step(q1), step(q2), step(q1)]
+    for _ in range(5):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and torch.equal(got[2], want[0])
+
+
+def test_attn_decode_given_buffers():
+    lens = [70, 500]
+    kc, vc, table = _cache("f32", lens, 16, 2, 64, seed=24)
+    q = _randn(_rng(3), 2, 4, 64)
+    want, _ = binding.delta_rule_attn_decode(q, kc, vc, table, _i32(lens))
+    ws = torch.full((binding.load().delta_rule_attn_decode_workspace_size(4, 2, 64, binding.DR_F32),), 255,
+                    dtype=torch.uint8, device="cuda")  # what it holds on entry does not matter
+    out = torch.full_like(q, float("nan"))
+    got, _ = binding.delta_rule_attn_decode(q, kc, vc, table, _i32(lens), out=out, workspace=ws)
+    torch.cuda.synchronize()
+    assert got.data_ptr() == out.data_ptr() and torch.equal(out, want)
+    small = torch.empty(256, dtype=torch.uint8, device="cuda")  # too small: one is allocated
+    assert torch.equal(binding.delta_rule_attn_decode(q, kc, vc, table, _i32(lens), workspace=small)[0], want)
+
+
+def test_python_level_refusals_on_cuda_tensors():
+    x = torch.zeros(4, 6, 64, device="cuda")
+    k, f, pos = torch.zeros(4, 2, 64, device="cuda"), _freq(64), _i32([0, 1, 2, 3])
+    w = torch.ones(64, device="cuda")
+    kc = torch.zeros(5, 16, 2, 64, device="cuda")
+    slots, table, lens = torch.zeros(4, dtype=torch.int64, device="cuda"), _i32([[0, 1]] * 4), _i32([3] * 4)
+    ok = dict(q=x, k=k, wq=w, wk=w, inv_freq=f, positions=pos)
+    binding.delta_rule_qkrope(**ok)
+    for bad in (dict(q=x.half()), dict(k=k.bfloat16()), dict(k=k[:3]), dict(wq=w[:32]), dict(wk=w.double()), dict(inv_freq=f.float()),
+                dict(positions=pos.long()), dict(positions=pos[:2]), dict(q=x.transpose(0, 1)), dict(k=k.cpu()), dict(wq=w.cpu()),
+                dict(q=x[0]), dict(positions=_i32([0] * 8)[::2])):
+        with pytest.raises(ValueError):
+            binding.delta_rule_qkrope(**{**ok, **bad})
+    for bad in (dict(inv_freq=f[:20]), dict(q=x[..., :32].contiguous(), k=k[..., :32].contiguous(), wq=None, wk=None, inv_freq=f[:16])):
+        with pytest.raises(binding.DeltaRuleError) as e:
+            binding.delta_rule_qkrope(**{**ok, **bad})
+        assert e.value.code == binding.DR_ERR_UNSUPPORTED
+    with pytest.raises(ValueError):
+        binding.delta_rule_qkrope_bwd(x, k, w, w, f, x[:3], k, pos)
+    with pytest.raises(ValueError):
+        binding.delta_rule_qkrope_bwd(x, k, w, w, f, x, k, pos, dq=x.bfloat16())
+    cache = dict(q=x, k=k, v=k, wq=w, wk=w, inv_freq=f, positions=pos, slots=slots, k_cache=kc, v_cache=kc.clone())
+    binding.delta_rule_qkrope_cache(**cache)
+    for bad in (dict(slots=slots.int()), dict(slots=slots[:2]), dict(positions=None), dict(v=x), dict(k_cache=kc[:, :8]),
+                dict(v_cache=kc[:4]), dict(k_cache=kc.bfloat16()), dict(q_out=x.transpose(0, 1).contiguous().transpose(0, 1))):
+        with pytest.raises(ValueError):
+            binding.delta_rule_qkrope_cache(**{**cache, **bad})
+    attn = dict(q=x, k_cache=kc, v_cache=kc, table=table, lens=lens)
+    binding.delta_rule_attn_decode(**attn)
+    for bad in (dict(q=x.bfloat16()), dict(table=table.long()), dict(table=table[:3]), dict(lens=lens[:3]), dict(lens=lens.long()),
+                dict(q=x[:, :, ::2]), dict(k_cache=kc.transpose(1, 2)), dict(v_cache=kc[:3]), dict(out=x.bfloat16()),
+                dict(workspace=x), dict(q=x[0]), dict(table=_i32([[0] * 4] * 4)[:, ::2])):
+        with pytest.raises(ValueError):
+            binding.delta_rule_attn_decode(**{**attn, **bad})
+    for bad, want in ((dict(q=x[:, :5].contiguous()), binding.DR_ERR_ARG), (dict(window=-1), binding.DR_ERR_ARG)):
+        with pytest.raises(binding.DeltaRuleError) as e:
+            binding.delta_rule_attn_decode(**{**attn, **bad})
+        assert e.value.code == want
+    with pytest.raises(TypeError):
+        binding.delta_rule_attn_decode(**{**attn, "scale": "a"})
+    pages = dict(cached=lens, fresh=lens, free_pages=_i32([1, 2]), n_free=_i32([2]), table=table, page=16, tokens=12)
+    for bad in (dict(cached=lens.long()), dict(fresh=lens[:2]), dict(n_free=_i32([1, 2])), dict(table=table[:2]), dict(tokens=-1),
+                dict(table=table[0]), dict(free_pages=_i32([[1]]))):
+        with pytest.raises(ValueError):
+            binding.delta_rule_pages(**{**pages, **bad})
+    with pytest.raises(binding.DeltaRuleError):
+        binding.delta_rule_pages(**{**pages, "page": 0})
+    torch.cuda.synchronize()
+
+
 # ------------------------------------------------------------------------------------ together
 @pytest.mark.parametrize("dtype,page", (("bf16", 16), ("f32", 7)))
 def test_serving_steps_together(dtype, page):
