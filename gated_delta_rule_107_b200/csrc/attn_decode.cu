@@ -9,7 +9,8 @@
 // What bounds it is reading the cache once: a key head's rows serve the G = Hq / Hk heads of its
 // group, 2 G flops a byte in bf16, far below what the tensor cores need to be busy; so the design
 // is about bytes in flight and an even split.
-//   Work.  The piece is a tile of 16 tokens of one (request, key head[, block of its query heads]).
+//   Work.  The piece is a tile of tokens of one (request, key head[, block of its query heads]): as
+//     many as make 4 KB of keys and 4 KB of values (8, 16 or 32).
 //     The tiles of all requests form one list, cut into equal contiguous runs, one per CTA, however
 //     ragged the lengths: a run may hold parts of several (request, head) segments.  A segment's
 //     start and join cost a CTA about as long as COST tiles, so each counts that much more in the
@@ -20,7 +21,7 @@
 //   Loads.  Each warp takes every fourth tile of its CTA's run through a pipeline of its own in
 //     shared memory, 16-byte asynchronous copies, rows swizzled by 16-byte chunk; the pipeline
 //     runs on across segments, and warps meet only at a segment's end.
-//   bf16.  The tile's tokens are the rows (M = 16) of mma.m16n8k16, the group's query heads its
+//   bf16.  The tile's tokens, 16 at a time, are the rows of mma.m16n8k16, the group's query heads its
 //     columns: S^T = K Q^T, then o^T = V^T P^T with P^T transposed in registers.  A group of up to
 //     8 heads is one n8 column block, of 16 two (larger groups are taken 16 heads at a time, and
 //     their rows read again for each block), so no row is spent on padding to 16 heads, and tcgen05's
@@ -28,8 +29,8 @@
 //     into two bf16 numbers (high and rest, 2^-17 of p) and multiplied twice: rounding P once
 //     would put as large an error in the output as its own rounding, and the second product is
 //     hidden behind the loads.
-//   fp32.  CUDA cores, 1, 2, 4 or up to 8 heads at a time: a lane holds half a token's channels for
-//     the scores, 1/32 of the channels of every head for the output.
+//   fp32.  CUDA cores, 1, 2, 4 or up to 8 heads at a time, packed arithmetic: a lane holds 32
+//     channels of one token for the scores, 1/32 of the channels of every head for the output.
 // Tokens that are masked (or whose table entry is no page) are neither read nor seen: their rows
 // in shared memory are zero-filled, their scores -inf.  A request with none gives o = 0, lse = -inf.
 #include <math_constants.h>
@@ -40,9 +41,10 @@
 namespace dr {
 namespace ad {
 
+using namespace dr::f32x2;
+
 constexpr int WARPS = 4, THREADS = WARPS * 32;
-constexpr int TILE = 16;          // tokens a warp takes at a time
-constexpr int MAX_CTAS = 296;     // two a SM (one where registers or shared memory hold no second)
+constexpr int MAX_CTAS = 296;     // two a SM
 constexpr int MIN_UNITS = WARPS;  // a CTA's run is at least one tile a warp
 #ifndef PROBE_COST
 #define PROBE_COST 4
@@ -59,6 +61,7 @@ struct Args {
     float scale2;
     FastDiv by_page;
     bool whole;          // a tile never crosses a page (the page is a multiple of the tile)
+    bool alike;          // both caches' pages are the same distance apart: one offset serves both
 };
 
 __device__ __forceinline__ uint32_t smem_u32(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
@@ -102,7 +105,7 @@ __device__ __forceinline__ float lse_of(float m, float l) { return l > 0.f ? (m 
 // The visible tokens of request r and its tiles.
 struct Span {
     int first, n, tile0, tiles;
-    __device__ __forceinline__ void set(const AttnDecode &a, int r) {
+    template <int TILE> __device__ __forceinline__ void set(const AttnDecode &a, int r) {
         const long long room = (long long)a.width * a.page;
         n = max(a.lens[r], 0);
         if (n > room) n = (int)room;
@@ -128,7 +131,7 @@ struct Run {
 };
 
 // All threads of the CTA; every CTA finds its run from the lengths alone.
-__device__ __forceinline__ Run find_run(const Args &x, int segs) {
+template <int TILE> __device__ __forceinline__ Run find_run(const Args &x, int segs) {
     __shared__ long long wsum[WARPS], found[2];
     const AttnDecode &a = x.a;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -136,7 +139,7 @@ __device__ __forceinline__ Run find_run(const Args &x, int segs) {
     long long mine = 0;
     Span sp;
     for (int r = b0; r < b1; ++r) {
-        sp.set(a, r);
+        sp.template set<TILE>(a, r);
         mine += units_of(sp) * segs;
     }
     long long inc = mine;
@@ -159,7 +162,7 @@ __device__ __forceinline__ Run find_run(const Args &x, int segs) {
     if (run.len > 0 && before <= run.u0 && run.u0 < before + mine) {
         int r = b0;
         for (; r < b1; ++r) {
-            sp.set(a, r);
+            sp.template set<TILE>(a, r);
             const long long w = units_of(sp) * segs;
             if (run.u0 < before + w) break;
             before += w;
@@ -176,7 +179,7 @@ __device__ __forceinline__ Run find_run(const Args &x, int segs) {
 constexpr int NOWHERE = 0x7fffffff;  // the unit of a place behind the list
 
 // moves `by` tiles on
-__device__ __forceinline__ void advance(Place &pl, int by, int segs, const AttnDecode &a) {
+template <int TILE> __device__ __forceinline__ void advance(Place &pl, int by, int segs, const AttnDecode &a) {
     pl.tile += by;
     pl.unit += by;
     while (pl.tile >= pl.sp.tiles) {
@@ -189,14 +192,15 @@ __device__ __forceinline__ void advance(Place &pl, int by, int segs, const AttnD
                     pl.unit = NOWHERE;
                     return;
                 }
-                pl.sp.set(a, pl.r);
+                pl.sp.template set<TILE>(a, pl.r);
             } while (pl.sp.tiles == 0);
         }
     }
 }
 
-// One warp's pipeline of tiles.  A stage is the K rows, then the V rows, of 16 tokens.
-template <typename E, int D, int STAGES> struct Pipe {
+// One warp's pipeline of tiles.  A stage is the K rows, then the V rows, of a tile.
+template <typename E, int D, int TILE_, int STAGES> struct Pipe {
+    static constexpr int TILE = TILE_;
     static constexpr int ROW = D * (int)sizeof(E), CPR = ROW / 16, E16 = 16 / (int)sizeof(E);  // bytes, 16-byte chunks of a row
     static constexpr int HALF = TILE * ROW, STAGE = 2 * HALF;
     static constexpr int RPI = 32 / (CPR < 32 ? CPR : 32);          // rows a warp copies with one instruction
@@ -206,14 +210,14 @@ template <typename E, int D, int STAGES> struct Pipe {
     // eight rows at one chunk lie in eight different banks groups
     static __device__ __forceinline__ uint32_t at(int r, int c) { return r * ROW + ((c ^ (r & 7)) << 4); }
 
-    // What a tile's copies need: the lane's token (lane % 16) is row `in` of page pg (-1: not seen;
+    // What a tile's copies need: the lane's token (lane % TILE) is row `in` of page pg (-1: not seen;
     // read ahead of the copies, since the table is a read of its own), key head h.
     struct Want {
         int pg, in, h;
     };
     static __device__ __forceinline__ Want want(const Args &x, const Place &pl) {
         const AttnDecode &a = x.a;
-        const int t = (pl.sp.tile0 + pl.tile) * TILE + (threadIdx.x & 15);
+        const int t = (pl.sp.tile0 + pl.tile) * TILE + (threadIdx.x & (TILE - 1));
         Want w = {-1, 0, pl.seg / x.RB};
         if (t >= pl.sp.first && t < pl.sp.n) {
             const int col = x.by_page.div(t);
@@ -221,25 +225,27 @@ template <typename E, int D, int STAGES> struct Pipe {
             w.in = t - col * a.page;
             w.pg = *at;
             // the entries that this CTA reads some tiles on
-            if ((threadIdx.x & 15) == 0 && col + AHEAD < a.width) asm volatile("prefetch.global.L2 [%0];" ::"l"(at + AHEAD));
+            if ((threadIdx.x & (TILE - 1)) == 0 && col + AHEAD < a.width) asm volatile("prefetch.global.L2 [%0];" ::"l"(at + AHEAD));
         }
         return w;
     }
     static constexpr int AHEAD = 128;
+    static constexpr uint32_t ALL = 0xffffffffu >> (32 - TILE);  // every token of a tile
 
     // copies the tile into the stage; returns the bits of its live tokens
     static __device__ __forceinline__ uint32_t load(uint32_t stage, const Args &x, const Want &w) {
         const AttnDecode &a = x.a;
         const int lane = threadIdx.x & 31;
         const bool seen = w.pg >= 0 && w.pg < a.n_pages;
-        const uint32_t live = __ballot_sync(0xffffffffu, seen) & 0xffffu;
+        const uint32_t live = __ballot_sync(0xffffffffu, seen) & ALL;
         const int c = lane % CPR, row0 = lane / CPR, e16 = E16;
         const size_t inside = ((size_t)w.in * a.Hk + w.h) * D;
-        const size_t ko = seen ? (size_t)w.pg * a.kps + inside : 0, vo = seen ? (size_t)w.pg * a.vps + inside : 0;
-        if (x.whole && live == 0xffffu) {  // 16 rows of one page: evenly spaced from the first one's
+        const size_t ko = seen ? (size_t)w.pg * a.kps + inside : 0;
+        if (x.whole && live == ALL) {  // rows of one page: evenly spaced from the first one's
             const size_t apart = (size_t)a.Hk * D;
             const E *k = (const E *)a.kc + __shfl_sync(0xffffffffu, ko, 0) + row0 * apart + c * e16;
-            const E *v = (const E *)a.vc + __shfl_sync(0xffffffffu, vo, 0) + row0 * apart + c * e16;
+            const size_t vo = x.alike ? 0 : (size_t)w.pg * a.vps + inside;
+            const E *v = (const E *)a.vc + __shfl_sync(0xffffffffu, x.alike ? ko : vo, 0) + row0 * apart + c * e16;
 #pragma unroll
             for (int i = 0; i < TILE; i += RPI) {
                 cp16(stage + at(i + row0, c), k + i * apart, true);
@@ -247,10 +253,11 @@ template <typename E, int D, int STAGES> struct Pipe {
             }
             return live;
         }
+        const size_t vo = seen && !x.alike ? (size_t)w.pg * a.vps + inside : 0;
 #pragma unroll
         for (int i = 0; i < TILE; i += RPI) {
             const int row = i + row0;
-            const size_t k = __shfl_sync(0xffffffffu, ko, row), v = __shfl_sync(0xffffffffu, vo, row);
+            const size_t k = __shfl_sync(0xffffffffu, ko, row), v = x.alike ? k : __shfl_sync(0xffffffffu, vo, row);
             const bool ok = live >> row & 1;
             cp16(stage + at(row, c), (const E *)a.kc + k + c * e16, ok);
             cp16(stage + HALF + at(row, c), (const E *)a.vc + v + c * e16, ok);
@@ -261,7 +268,8 @@ template <typename E, int D, int STAGES> struct Pipe {
 
 // ------------------------------------------------------------------ one warp's arithmetic
 // Each keeps, for the heads of a block, m (base 2), l and o, and offers
-//   fetch(q row of the block's first head, heads): reads the queries; begin(): they are the ones from now
+//   fetch(q row of the block's first head, heads): reads the queries; share(place in shared memory),
+//     where warps share them; begin(): they are the ones from now
 //   tile(stage, live)
 //   finish(m, l, o): l summed over lanes, all three to shared memory, o as [head][slot_of(head, channel)]
 
@@ -271,8 +279,8 @@ __device__ __forceinline__ int slot_of(int head, int ch) { return ch ^ ((head >>
 
 template <int D, int NT> struct Mma {  // bf16: blocks of 8 NT heads
     typedef __nv_bfloat16 E;
-    static constexpr int GB = 8 * NT, STAGES = (D == 128 ? 3 : 6), CTAS = MAX_CTAS;
-    typedef Pipe<E, D, STAGES> P;
+    static constexpr int GB = 8 * NT, STAGES = 3, CTAS = MAX_CTAS, SUB = 128 / D;  // 16 SUB tokens a tile
+    typedef Pipe<E, D, 16 * SUB, STAGES> P;
     uint32_t q[D / 16][NT][2], qn[D / 16][NT][2];
     float o[D / 16][NT][4], m[NT][2], l[NT][2];
 
@@ -303,35 +311,45 @@ template <int D, int NT> struct Mma {  // bf16: blocks of 8 NT heads
     }
     __device__ __forceinline__ void tile(uint32_t stage, uint32_t live, float scale2, void *) {
         const int lane = threadIdx.x & 31, g = lane >> 2;
-        // scores of token g (0, 1) and g + 8 (2, 3), heads 2 t and 2 t + 1 of each block of 8; two
+        // scores of token g (0, 1) and g + 8 (2, 3) of 16, heads 2 t and 2 t + 1 of each block of 8; two
         // accumulators, so that half as many products wait on one another
-        float s[NT][4], s1[NT][4];
+        float s[SUB][NT][4];
+#pragma unroll
+        for (int u = 0; u < SUB; ++u) {
+            float s1[NT][4];
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) s[u][j][i] = s1[j][i] = 0.f;
+#pragma unroll
+            for (int k = 0; k < D / 16; k += 2) {
+                uint32_t a[4], b[4];
+                ldsm4(a, stage + P::at(u * 16 + (lane & 15), k * 2 + (lane >> 4)));
+                ldsm4(b, stage + P::at(u * 16 + (lane & 15), k * 2 + 2 + (lane >> 4)));
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+                    mma(s[u][j], a, q[k][j][0], q[k][j][1]);
+                    mma(s1[j], b, q[k + 1][j][0], q[k + 1][j][1]);
+                }
+            }
+            const bool lo = live >> (u * 16 + g) & 1, hi = live >> (u * 16 + g + 8) & 1;
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    s[u][j][i] = lo ? (s[u][j][i] + s1[j][i]) * scale2 : -CUDART_INF_F;
+                    s[u][j][i + 2] = hi ? (s[u][j][i + 2] + s1[j][i + 2]) * scale2 : -CUDART_INF_F;
+                }
+        }
+        float mx[NT][2];
 #pragma unroll
         for (int j = 0; j < NT; ++j)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) s[j][i] = s1[j][i] = 0.f;
-#pragma unroll
-        for (int k = 0; k < D / 16; k += 2) {
-            uint32_t a[4], b[4];
-            ldsm4(a, stage + P::at(lane & 15, k * 2 + (lane >> 4)));
-            ldsm4(b, stage + P::at(lane & 15, k * 2 + 2 + (lane >> 4)));
-#pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                mma(s[j], a, q[k][j][0], q[k][j][1]);
-                mma(s1[j], b, q[k + 1][j][0], q[k + 1][j][1]);
-            }
-        }
-        const bool lo = live >> g & 1, hi = live >> (g + 8) & 1;
-        float mx[NT][2];
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-#pragma unroll
             for (int i = 0; i < 2; ++i) {
-                s[j][i] = lo ? (s[j][i] + s1[j][i]) * scale2 : -CUDART_INF_F;
-                s[j][i + 2] = hi ? (s[j][i + 2] + s1[j][i + 2]) * scale2 : -CUDART_INF_F;
-                mx[j][i] = fmaxf(s[j][i], s[j][i + 2]);
+                mx[j][i] = fmaxf(s[0][j][i], s[0][j][i + 2]);
+#pragma unroll
+                for (int u = 1; u < SUB; ++u) mx[j][i] = fmaxf(mx[j][i], fmaxf(s[u][j][i], s[u][j][i + 2]));
             }
-        }
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1)
 #pragma unroll
@@ -358,39 +376,43 @@ template <int D, int NT> struct Mma {  // bf16: blocks of 8 NT heads
                     }
                 }
         }
-        uint32_t ph[NT][2], pl[NT][2];
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-            float p[4], rest[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                // -inf minus -inf (nothing seen yet) must not be NaN
-                p[i] = s[j][i] == -CUDART_INF_F ? 0.f : ex2(s[j][i] - m[j][i & 1]);
-                l[j][i & 1] += p[i];
-            }
-            ph[j][0] = pack(p[0], p[1]);
-            ph[j][1] = pack(p[2], p[3]);
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                rest[2 * i] = p[2 * i] - __uint_as_float(ph[j][i] << 16);
-                rest[2 * i + 1] = p[2 * i + 1] - __uint_as_float(ph[j][i] & 0xFFFF0000u);
-                pl[j][i] = trans8(pack(rest[2 * i], rest[2 * i + 1]));
-                ph[j][i] = trans8(ph[j][i]);
-            }
-        }
-        const uint32_t v = stage + P::HALF;
         const int row = (lane & 7) + ((lane >> 4) << 3), c0 = lane >> 3 & 1;
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-            uint32_t a[4];
-            ldsm4t(a, v + P::at(row, 2 * k + c0));
+        for (int u = 0; u < SUB; ++u) {
+            uint32_t ph[NT][2], pl[NT][2];
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
-                mma(o[k][j], a, ph[j][0], ph[j][1]);
-                mma(o[k][j], a, pl[j][0], pl[j][1]);
+                float p[4], rest[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    // -inf minus -inf (nothing seen yet) must not be NaN
+                    p[i] = s[u][j][i] == -CUDART_INF_F ? 0.f : ex2(s[u][j][i] - m[j][i & 1]);
+                    l[j][i & 1] += p[i];
+                }
+                ph[j][0] = pack(p[0], p[1]);
+                ph[j][1] = pack(p[2], p[3]);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    rest[2 * i] = p[2 * i] - __uint_as_float(ph[j][i] << 16);
+                    rest[2 * i + 1] = p[2 * i + 1] - __uint_as_float(ph[j][i] & 0xFFFF0000u);
+                    pl[j][i] = trans8(pack(rest[2 * i], rest[2 * i + 1]));
+                    ph[j][i] = trans8(ph[j][i]);
+                }
+            }
+            const uint32_t v = stage + P::HALF;
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+                uint32_t a[4];
+                ldsm4t(a, v + P::at(u * 16 + row, 2 * k + c0));
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+                    mma(o[k][j], a, ph[j][0], ph[j][1]);
+                    mma(o[k][j], a, pl[j][0], pl[j][1]);
+                }
             }
         }
     }
+    __device__ __forceinline__ void share(float *) {}
     __device__ __forceinline__ void finish(float *sm, float *sl, float *so) {
         const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
 #pragma unroll
@@ -411,85 +433,99 @@ template <int D, int NT> struct Mma {  // bf16: blocks of 8 NT heads
                 }
             }
     }
-    static constexpr int EXTRA = 0;  // bytes of shared memory of the warp's own
+    static constexpr int EXTRA = 0, SHARED = 0;  // bytes of shared memory: of the warp's own, of the CTA's warps together
 };
 
 template <int D, int H> struct Simt {  // fp32: blocks of H heads, at most 8
     typedef float E;
-    static constexpr int GB = H, STAGES = 3, CTAS = D == 128 ? MAX_CTAS / 2 : MAX_CTAS, NC = D / 32;
-    typedef Pipe<E, D, STAGES> P;
-    float o[GB][NC], m[GB], l[GB];
-    static constexpr int EXTRA = (GB * D + TILE * GB) * 4;  // the block's queries, the tile's p
+    static constexpr int GB = H, STAGES = 3, CTAS = MAX_CTAS, NC = D / 32, TILE = 1024 / D;
+    typedef Pipe<E, D, TILE, STAGES> P;
+    f2 o[GB][NC / 2];
+    float m[GB], l[GB], qn[GB * D / THREADS > 0 ? GB * D / THREADS : 1];
+    static constexpr int EXTRA = TILE * GB * 8;  // the tile's p, each twice (one packed operand)
+    static constexpr int SHARED = GB * D * 4;    // the block's queries
+    f2 *ps;
+    const float *qs;
 
-    float *qs, *ps, qn[GB * D / 32];
+    // the queries are read by all threads together, and shared by the warps
     __device__ __forceinline__ void fetch(const E *src, int heads) {
-        const int lane = threadIdx.x & 31;
 #pragma unroll
-        for (int i = 0; i < GB * D / 32; ++i) qn[i] = (i * 32 + lane) / D < heads ? src[i * 32 + lane] : 0.f;
+        for (int i = 0; i < (GB * D + THREADS - 1) / THREADS; ++i) {
+            const int at = i * THREADS + threadIdx.x;
+            qn[i] = at < heads * D ? src[at] : 0.f;
+        }
+    }
+    __device__ __forceinline__ void share(float *to) {
+#pragma unroll
+        for (int i = 0; i < (GB * D + THREADS - 1) / THREADS; ++i) {
+            const int at = i * THREADS + threadIdx.x;
+            if (at < GB * D) to[at] = qn[i];
+        }
+        qs = to;
     }
     __device__ __forceinline__ void begin() {
-        const int lane = threadIdx.x & 31;
-        __syncwarp();
-#pragma unroll
-        for (int i = 0; i < GB * D / 32; ++i) qs[i * 32 + lane] = qn[i];
-        __syncwarp();
 #pragma unroll
         for (int h = 0; h < GB; ++h) {
             m[h] = -CUDART_INF_F;
             l[h] = 0.f;
 #pragma unroll
-            for (int c = 0; c < NC; ++c) o[h][c] = 0.f;
+            for (int c = 0; c < NC / 2; ++c) o[h][c] = 0;
         }
     }
     __device__ __forceinline__ void tile(uint32_t, uint32_t live, float scale2, const char *base) {
-        const int lane = threadIdx.x & 31, t = lane & 15, half = lane >> 4;
-        float s[GB] = {};
+        const int lane = threadIdx.x & 31, t = lane & (TILE - 1), part = lane / TILE;
+        f2 s2[GB] = {};
 #pragma unroll 4
-        for (int c = 0; c < D / 8; ++c) {
-            const int ch = half * (D / 8) + c;
+        for (int c = 0; c < 8; ++c) {  // the lane's 32 channels
+            const int ch = part * 8 + c;
             const float4 k = *reinterpret_cast<const float4 *>(base + P::at(t, ch));
+            const f2 k0 = mk(k.x, k.y), k1 = mk(k.z, k.w);
 #pragma unroll
             for (int h = 0; h < GB; ++h) {
                 const float4 q = *reinterpret_cast<const float4 *>(qs + h * D + 4 * ch);
-                s[h] += k.x * q.x + k.y * q.y + k.z * q.z + k.w * q.w;
+                s2[h] = fma(k0, mk(q.x, q.y), s2[h]);
+                s2[h] = fma(k1, mk(q.z, q.w), s2[h]);
             }
         }
         const bool ok = live >> t & 1;
-        float f[GB];
 #pragma unroll
         for (int h = 0; h < GB; ++h) {
-            s[h] += __shfl_xor_sync(0xffffffffu, s[h], 16);
-            s[h] = ok ? s[h] * scale2 : -CUDART_INF_F;
-            float mx = s[h];
+            float s = sum2(s2[h]);
 #pragma unroll
-            for (int d = 1; d < 16; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+            for (int d = TILE; d < 32; d <<= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+            s = ok ? s * scale2 : -CUDART_INF_F;
+            float mx = s;
+#pragma unroll
+            for (int d = 1; d < TILE; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
             const float mn = fmaxf(m[h], mx);
-            f[h] = m[h] == mn ? 1.f : ex2(m[h] - mn);
+            const float f = m[h] == mn ? 1.f : ex2(m[h] - mn);
             m[h] = mn;
-            const float p = s[h] == -CUDART_INF_F ? 0.f : ex2(s[h] - mn);
-            l[h] = l[h] * f[h] + (half == 0 ? p : 0.f);  // each token counts once over the warp
-            if (half == 0) ps[t * GB + h] = p;
+            const float p = s == -CUDART_INF_F ? 0.f : ex2(s - mn);
+            l[h] = l[h] * f + (part == 0 ? p : 0.f);  // each token counts once over the warp
+            if (part == 0) ps[t * GB + h] = mk(p, p);
+            const f2 ff = mk(f, f);
 #pragma unroll
-            for (int c = 0; c < NC; ++c) o[h][c] *= f[h];
+            for (int c = 0; c < NC / 2; ++c) o[h][c] = mul(o[h][c], ff);
         }
         __syncwarp();
         const char *v = base + P::HALF;
 #pragma unroll 4
         for (int u = 0; u < TILE; ++u) {
-            float x[NC];
+            f2 x[NC / 2];
             const char *at = v + P::at(u, lane * NC / 4) + (lane * NC % 4) * 4;
-            if (NC == 4) {
+            if constexpr (NC == 4) {
                 const float4 y = *reinterpret_cast<const float4 *>(at);
-                x[0] = y.x; x[1] = y.y; x[NC - 2] = y.z; x[NC - 1] = y.w;
+                x[0] = mk(y.x, y.y);
+                x[1] = mk(y.z, y.w);
             } else {
                 const float2 y = *reinterpret_cast<const float2 *>(at);
-                x[0] = y.x; x[1] = y.y;
+                x[0] = mk(y.x, y.y);
             }
 #pragma unroll
             for (int h = 0; h < GB; ++h) {
-                const float p = ps[u * GB + h];
+                const f2 p = ps[u * GB + h];
 #pragma unroll
-                for (int c = 0; c < NC; ++c) o[h][c] += p * x[c];
+                for (int c = 0; c < NC / 2; ++c) o[h][c] = fma(p, x[c], o[h][c]);
             }
         }
         __syncwarp();  // ps is free for the next tile
@@ -504,18 +540,18 @@ template <int D, int H> struct Simt {  // fp32: blocks of H heads, at most 8
                 sl[h] = l[h];
             }
 #pragma unroll
-            for (int c = 0; c < NC; ++c) so[h * D + slot_of(h, lane * NC + c)] = o[h][c];
+            for (int c = 0; c < NC / 2; ++c) *reinterpret_cast<f2 *>(so + h * D + slot_of(h, lane * NC + 2 * c)) = o[h][c];
         }
     }
 };
 
 template <class C, int D> constexpr int warp_bytes() { return C::STAGES * C::P::STAGE + C::EXTRA; }
-template <class C, int D> constexpr int smem_bytes() { return WARPS * warp_bytes<C, D>(); }
+template <class C, int D> constexpr int smem_bytes() { return WARPS * warp_bytes<C, D>() + C::SHARED; }
 
 template <class C, int D> __global__ void __launch_bounds__(THREADS) k_attn(const Args x) {
     typedef typename C::E E;
     typedef typename C::P P;
-    constexpr int GB = C::GB, STAGES = C::STAGES;
+    constexpr int GB = C::GB, STAGES = C::STAGES, TILE = P::TILE;
     extern __shared__ __align__(128) char smem[];
     __shared__ float sm_m[WARPS][GB], sm_l[WARPS][GB];
     __shared__ int sm_at[WARPS];
@@ -525,10 +561,10 @@ template <class C, int D> __global__ void __launch_bounds__(THREADS) k_attn(cons
     const int segs = a.Hk * x.RB;
     let_next();  // k_attn_join: small blocks, wanted at once
     after_previous();
-    const Run run = find_run(x, segs);
+    const Run run = find_run<TILE>(x, segs);
     for (int r = blockIdx.x; r < a.R; r += gridDim.x) {  // requests that see nothing
-        Span sp;
-        sp.set(a, r);
+        Span sp = {};
+        sp.template set<TILE>(a, r);
         if (sp.tiles > 0) continue;
         for (int i = tid; i < a.Hq * D; i += THREADS) ((E *)a.out)[(size_t)r * a.Hq * D + i] = from_f<E>(0.f);
         if (a.lse)
@@ -539,7 +575,7 @@ template <class C, int D> __global__ void __launch_bounds__(THREADS) k_attn(cons
     here.unit = NOWHERE;
     if (run.len > 0) {
         here.r = run.r0;
-        here.sp.set(a, here.r);
+        here.sp.template set<TILE>(a, here.r);
         const long long in = run.u0 - run.base;  // not negative, inside request r0
         here.seg = (int)(in / units_of(here.sp));
         const int off = (int)(in - here.seg * units_of(here.sp)) - COST;
@@ -561,7 +597,7 @@ template <class C, int D> __global__ void __launch_bounds__(THREADS) k_attn(cons
     bool there[STAGES];
 #pragma unroll
     for (int i = 0; i < STAGES; ++i) {
-        if (next.unit < run.len) advance(next, i == 0 ? warp : WARPS, segs, a);
+        if (next.unit < run.len) advance<TILE>(next, i == 0 ? warp : WARPS, segs, a);
         there[i] = next.unit < run.len;
         if (there[i]) ahead[i] = P::want(x, next);
     }
@@ -580,16 +616,16 @@ template <class C, int D> __global__ void __launch_bounds__(THREADS) k_attn(cons
     bool comes = there[STAGES - 1];
 
     C c;
-    if constexpr (C::EXTRA > 0) {
-        c.qs = reinterpret_cast<float *>(mine + STAGES * P::STAGE);
-        c.ps = c.qs + GB * D;
-    }
+    if constexpr (C::EXTRA > 0) c.ps = reinterpret_cast<f2 *>(mine + STAGES * P::STAGE);
+    float *together = reinterpret_cast<float *>(smem + WARPS * warp_bytes<C, D>());
     int done = 0, mytile = warp;  // the run's tiles before the current segment; the warp's next one
     auto fetch = [&](const Place &pl) {
         const int h = pl.seg / x.RB, rb = pl.seg - h * x.RB;
         c.fetch((const E *)a.q + ((size_t)pl.r * a.Hq + h * x.G + rb * GB) * D, min(GB, x.G - rb * GB));
     };
     fetch(here);
+    c.share(together);
+    if (C::SHARED > 0) __syncthreads();
     for (int part = 0; here.unit < run.len; ++part) {
         const int h = here.seg / x.RB, rb = here.seg - h * x.RB, head0 = h * x.G + rb * GB;
         const int heads = min(GB, x.G - rb * GB);
@@ -601,7 +637,7 @@ template <class C, int D> __global__ void __launch_bounds__(THREADS) k_attn(cons
             __syncwarp();
             const uint32_t bits = lives[warp][got];
             issue(coming, comes);
-            if (comes) advance(next, WARPS, segs, a);
+            if (comes) advance<TILE>(next, WARPS, segs, a);
             comes = next.unit < run.len;
             if (comes) coming = P::want(x, next);
             c.tile(stages + got * P::STAGE, bits, x.scale2, mine + got * P::STAGE);
@@ -610,12 +646,13 @@ template <class C, int D> __global__ void __launch_bounds__(THREADS) k_attn(cons
         }
         // the queries of the segment behind this one, while the warps join
         Place then = here;
-        advance(then, rest, segs, a);
+        advance<TILE>(then, rest, segs, a);
         if (then.unit < run.len) fetch(then);
         // each warp's o goes to the stage that it will fill next, and which holds nothing now
         c.finish(sm_m[warp], sm_l[warp], reinterpret_cast<float *>(mine + put * P::STAGE));
         if (lane == 0) sm_at[warp] = warp * warp_bytes<C, D>() + put * P::STAGE;
-        __syncthreads();
+        __syncthreads();  // all warps are done with the segment
+        c.share(together);
         const size_t slot = 2 * blockIdx.x + (part > 0);
         for (int i = tid; i < heads * (D / 8); i += THREADS) {
             const int hd = i / (D / 8), ch = (i - hd * (D / 8)) * 8;
@@ -710,11 +747,12 @@ template <class C, int D> static cudaError_t launch(Args x, cudaStream_t s) {
     x.head = (int4 *)a.ws;
     x.ml = (float2 *)(x.head + MAX_CTAS);
     x.part = (float *)(x.ml + 2 * MAX_CTAS * C::GB);  // 16-byte aligned
+    x.whole = a.page % C::P::TILE == 0;
     const int smem = smem_bytes<C, D>();
     cudaError_t e = cudaFuncSetAttribute(k_attn<C, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     // no more CTAs than the tables have room for runs
-    const double tiles = (double)a.R * a.Hk * x.RB * ((double)a.width * a.page / TILE + 1 + COST);
+    const double tiles = (double)a.R * a.Hk * x.RB * ((double)a.width * a.page / C::P::TILE + 1 + COST);
     const int ctas = tiles / MIN_UNITS < C::CTAS - 1 ? (int)(tiles / MIN_UNITS) + 1 : C::CTAS;
     e = launch_after(k_attn<C, D>, dim3(ctas), dim3(THREADS), smem, s, x);
     if (e != cudaSuccess) return e;
@@ -744,7 +782,7 @@ cudaError_t attn_decode_run(const AttnDecode &p, bool bf16, cudaStream_t s) {
     x.G = p.Hq / p.Hk;
     x.scale2 = p.scale * ad::LOG2E;
     x.by_page = FastDiv(p.page);
-    x.whole = p.page % ad::TILE == 0;
+    x.alike = p.kps == p.vps;
     const int GB = ad::heads_per_block(x.G, bf16);
     if (!bf16) return p.d == 128 ? ad::simt<128>(x, GB, s) : ad::simt<64>(x, GB, s);
     if (p.d == 128)

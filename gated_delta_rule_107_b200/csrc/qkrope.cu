@@ -29,35 +29,7 @@ constexpr long long WARPS_WANTED = 16 * 148;
 constexpr int BWD_CTAS = 2 * 148;         // one wave; they are also the number of its partial sums
 constexpr double INV_2PI = 0.15915494309189533577;
 
-// Two fp32 numbers in a 64-bit register pair: Blackwell's packed arithmetic takes one issue slot
-// for both, and these kernels are bound by issue slots once their loads are far enough ahead.
-typedef unsigned long long f2;
-__device__ __forceinline__ f2 mk(float lo, float hi) {
-    f2 d;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
-    return d;
-}
-__device__ __forceinline__ void un(f2 x, float &lo, float &hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(x)); }
-__device__ __forceinline__ f2 mul(f2 a, f2 b) {
-    f2 d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-__device__ __forceinline__ f2 fma(f2 a, f2 b, f2 c) {
-    f2 d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-    return d;
-}
-__device__ __forceinline__ f2 sub(f2 a, f2 b) {
-    f2 d;
-    asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-__device__ __forceinline__ float sum2(f2 x) {
-    float a, b;
-    un(x, a, b);
-    return a + b;
-}
+using namespace dr::f32x2;
 
 // The lanes of a token and what a lane holds of each row: two 16-byte vectors (indexes ia, ib),
 // chosen so that the two channels of each pair meet in the lane, as VEC first and VEC second
