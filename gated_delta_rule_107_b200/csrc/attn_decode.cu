@@ -46,10 +46,7 @@ using namespace dr::f32x2;
 constexpr int WARPS = 4, THREADS = WARPS * 32;
 constexpr int MAX_CTAS = 296;     // two a SM
 constexpr int MIN_UNITS = WARPS;  // a CTA's run is at least one tile a warp
-#ifndef PROBE_COST
-#define PROBE_COST 4
-#endif
-constexpr int COST = PROBE_COST;           // of a segment, in tiles
+constexpr int COST = 6;           // of a segment, in tiles (64 requests of 1 to 500 tokens, 8 key heads: 22 us; 4: 24, 2: 29)
 constexpr float LOG2E = 1.44269504088896340736f, LN2 = 0.69314718055994530942f;
 
 struct Args {
@@ -60,6 +57,7 @@ struct Args {
     int4 *head;          // [MAX_CTAS]: the split segment that begins in a CTA: request, key head, block, last CTA
     float scale2;
     FastDiv by_page;
+    double inv_ctas;     // 1 / CTAs
     bool whole;          // a tile never crosses a page (the page is a multiple of the tile)
     bool alike;          // both caches' pages are the same distance apart: one offset serves both
 };
@@ -130,6 +128,23 @@ struct Run {
     int len, per, r0;
 };
 
+// total / CTAs, rounded up (a 64-bit division takes a third of a microsecond): the product is off by
+// less than one
+__device__ __forceinline__ int per_cta(long long total, double inv_ctas) {
+    const long long n = gridDim.x;
+    long long q = (long long)((double)total * inv_ctas);
+    q -= q * n >= total && q > 0;
+    while (q * n < total) ++q;
+    return (int)q;
+}
+// in / units for a small quotient
+__device__ __forceinline__ int small_quotient(long long in, long long units) {
+    int q = (int)__fdividef((float)in, (float)units);
+    while ((long long)(q + 1) * units <= in) ++q;
+    while ((long long)q * units > in) --q;
+    return q;
+}
+
 // All threads of the CTA; every CTA finds its run from the lengths alone.
 template <int TILE> __device__ __forceinline__ Run find_run(const Args &x, int segs) {
     __shared__ long long wsum[WARPS], found[2];
@@ -156,7 +171,7 @@ template <int TILE> __device__ __forceinline__ Run find_run(const Args &x, int s
         total += wsum[w];
     }
     Run run;
-    run.per = (int)max((long long)MIN_UNITS, (total + gridDim.x - 1) / gridDim.x);
+    run.per = max(MIN_UNITS, per_cta(total, x.inv_ctas));
     run.u0 = min(total, (long long)run.per * blockIdx.x);
     run.len = (int)min(total - run.u0, (long long)run.per);
     if (run.len > 0 && before <= run.u0 && run.u0 < before + mine) {
@@ -577,7 +592,7 @@ template <class C, int D> __global__ void __launch_bounds__(THREADS) k_attn(cons
         here.r = run.r0;
         here.sp.template set<TILE>(a, here.r);
         const long long in = run.u0 - run.base;  // not negative, inside request r0
-        here.seg = (int)(in / units_of(here.sp));
+        here.seg = small_quotient(in, units_of(here.sp));
         const int off = (int)(in - here.seg * units_of(here.sp)) - COST;
         here.tile = max(off, 0);
         here.unit = max(-off, 0);
@@ -754,6 +769,7 @@ template <class C, int D> static cudaError_t launch(Args x, cudaStream_t s) {
     // no more CTAs than the tables have room for runs
     const double tiles = (double)a.R * a.Hk * x.RB * ((double)a.width * a.page / C::P::TILE + 1 + COST);
     const int ctas = tiles / MIN_UNITS < C::CTAS - 1 ? (int)(tiles / MIN_UNITS) + 1 : C::CTAS;
+    x.inv_ctas = 1.0 / ctas;
     e = launch_after(k_attn<C, D>, dim3(ctas), dim3(THREADS), smem, s, x);
     if (e != cudaSuccess) return e;
     return launch_after(k_attn_join<typename C::E, D>, dim3(ctas, x.G < C::GB ? x.G : C::GB), dim3(256), 0, s, x);
