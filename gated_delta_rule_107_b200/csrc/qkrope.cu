@@ -523,8 +523,7 @@ template <typename E, int D, bool INTER> static cudaError_t fwd(const QkRope &p,
     const dim3 grid((unsigned)min((groups + WARPS - 1) / WARPS, 1ll << 20), (unsigned)((heads + hpg - 1) / hpg));
     auto go = [&](auto kern) -> cudaError_t {
         constexpr int smem = Ring<2, PF_FWD>::WARP_BYTES * (THREADS / 32);
-        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-        if (e != cudaSuccess) return e;
+        static_assert(smem + sizeof(Shared<E, D, INTER>) <= 48 * 1024, "fits without an opt-in");
         return launch_after(kern, grid, dim3(THREADS), smem, s, p, hpg);
     };
     return cache ? go(k_qkrope<E, D, INTER, true>) : go(k_qkrope<E, D, INTER, false>);

@@ -161,8 +161,19 @@ PyObject *pages(PyObject *, Args a, Py_ssize_t n) {
          *sp = dense(stack, "free_pages", at::kInt, dev, -1), *np = dense(n_free, "n_free", at::kInt, dev, 1),
          *tp = dense(table, "table", at::kInt, dev, -1);
     On on(dev);
-    at::Tensor lens = empty({R}, at::kInt, dev), cu = empty({R + 1}, at::kInt, dev), pos = empty({N}, at::kInt, dev),
-               left = empty({1}, at::kInt, dev), slots = empty({N}, at::kLong, dev);
+    // the five outputs side by side in one allocation (five take 2 us more), the 8-byte ones first
+    const at::Tensor all = empty({12ll * N + 8ll * R + 8}, at::kByte, dev);
+    int64_t at = 0;
+    auto next = [&](at::ScalarType type, int64_t n) {
+        auto t = c10::make_intrusive<c10::TensorImpl>(c10::Storage(all.storage()), all.key_set(), c10::scalarTypeToTypeMeta(type));
+        const int64_t size = (int64_t)c10::elementSize(type);
+        t->set_storage_offset(all.storage_offset() + at / size);
+        t->set_sizes_contiguous(n);
+        at += n * size;
+        return at::Tensor(std::move(t));
+    };
+    const at::Tensor slots = next(at::kLong, N), pos = next(at::kInt, N), lens = next(at::kInt, R), cu = next(at::kInt, R + 1ll),
+                     left = next(at::kInt, 1);
     const int rc = c_pages((int *)cp, (int *)fp, (int *)sp, (int *)np, (int *)tp, (int *)lens.data_ptr(), (int *)cu.data_ptr(),
                            (int *)pos.data_ptr(), (long long *)slots.data_ptr(), (int *)left.data_ptr(), R,
                            extent(stack.numel(), "free_pages"), extent(table.size(1), "table"), page, N, on.stream);
