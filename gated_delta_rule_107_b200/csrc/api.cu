@@ -979,6 +979,7 @@ extern "C" int delta_rule_attn_decode(const void *q, const void *k_cache, const 
     int rc = check_attn(Hq, Hk, d, dtype);
     if (rc != DR_OK) return rc;
     if (R < 0 || n_pages < 0 || page <= 0 || width < 0 || window < 0) return DR_ERR_ARG;
+    if ((double)R * Hq * ((double)width * page + 64) >= 2199023255552.0) return DR_ERR_UNSUPPORTED;  // the split counts in 32 bits a CTA
     if (R == 0) return DR_OK;
     if (!q || !lens || !out || (width > 0 && !table) || (n_pages > 0 && (!k_cache || !v_cache))) return DR_ERR_ARG;
     rc = check_stride(k_page_stride, (long long)page * Hk * d, dtype);

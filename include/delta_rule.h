@@ -461,10 +461,11 @@ int delta_rule_qkrope_cache(const void *q, const void *k, const void *v, const f
  *     s_t = scale q . k_t  over t in [max(0, lens[r] - window), lens[r])
  *     out [R,Hq,d] = sum_t e^{s_t} v_t / sum_t e^{s_t},  lse [R,Hq] = log sum_t e^{s_t}
  * (lse fp32, NULL = not written; window = 0: all tokens).  A request that sees no
- * token gets out = 0, lse = -inf.  Tokens behind the table's width, and tokens
+ * token, or only scores of -inf, gets out = 0, lse = -inf.  Tokens behind the table's width, and tokens
  * whose table entry is no page (outside [0, n_pages)), are not seen; what their
  * rows hold is not read.  Sums and softmax statistics are fp32.  Results do not
- * change from run to run.  The workspace is
+ * change from run to run.  R * Hq * (width * page + 64) must stay below 2^41
+ * (DR_ERR_UNSUPPORTED).  The workspace is
  * delta_rule_attn_decode_workspace_size(Hq, Hk, d, dtype) bytes (whatever the
  * lengths; (size_t)-1 for invalid arguments), 256-byte aligned.
  */

@@ -178,6 +178,7 @@ def test_attn_decode_refusals(lib):
                 dict(window=-1), dict(dtype=3), dict(kps=2048), dict(vps=2048)):
         assert call(**bad) == b.DR_ERR_ARG, bad
     assert call(d=96) == b.DR_ERR_UNSUPPORTED and call(kps=4100) == b.DR_ERR_ALIGN
+    assert call(R=1 << 20, width=1 << 18, page=16) == b.DR_ERR_UNSUPPORTED
     need = lib.delta_rule_attn_decode_workspace_size(8, 2, 128, b.DR_BF16)
     assert call(ws=None) == b.DR_ERR_WORKSPACE and call(nws=need - 1) == b.DR_ERR_WORKSPACE
     assert call(ws=A + 16) == b.DR_ERR_ALIGN

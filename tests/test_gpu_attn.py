@@ -429,6 +429,10 @@ def test_attn_decode_scales_and_extreme_scores(dtype):
     o, lse = binding.delta_rule_attn_decode(q, kc, vc, table, _i32(lens), want_lse=True)
     torch.cuda.synchronize()
     _check_attn(o, lse, q, kc, vc, table, lens, dtype, what="a score of -inf")
+    kc[table[0, :5].long()] = float("-inf")  # every visible score is -inf: as a request that sees nothing
+    o, lse = binding.delta_rule_attn_decode(q, kc, vc, table, _i32([70, 130]), want_lse=True)
+    torch.cuda.synchronize()
+    assert (o[0] == 0).all() and torch.isneginf(lse[0]).all() and o[1].isfinite().all()
     vc[table[1, 2], 1] = float("nan")  # a visible NaN is not hidden, and stays in its request
     o, lse = binding.delta_rule_attn_decode(q, kc, vc, table, _i32(lens), want_lse=True)
     torch.cuda.synchronize()
@@ -522,6 +526,43 @@ def test_attn_decode_behind_copies_in_a_graph():
         graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and torch.equal(got[2], want[0])
+
+
+def test_captured_across_streams_and_replayed_at_once():
+    """One capture that forks to a second stream and joins again, and two graphs replayed on two streams."""
+    lens = [2500, 1, 60, 800]
+    kc, vc, table = _cache("bf16", lens, 16, 2, 64, seed=25)
+    q, ln = _randn(_rng(1), 4, 8, 64, dtype="bf16"), _i32(lens)
+    x, k, _, (wq, wk), f, pos = _qk_case("bf16", 2, 300, 4, 2, 64, 64, seed=26)
+    gq, gk = _randn(_rng(2), 2, 300, 4, 64, dtype="bf16"), _randn(_rng(3), 2, 300, 2, 64, dtype="bf16")
+
+    def both(side):
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            o = binding.delta_rule_attn_decode(q, kc, vc, table, ln, want_lse=True)
+        y = binding.delta_rule_qkrope(x, k, wq, wk, f, pos)
+        g = binding.delta_rule_qkrope_bwd(x, k, wq, wk, f, gq, gk, pos)
+        main.wait_stream(side)
+        o2 = binding.delta_rule_attn_decode(q, kc, vc, table, ln, want_lse=True)  # behind both branches
+        return (*o, *y, *g, *o2)
+
+    want = [t.clone() for t in both(torch.cuda.Stream())]
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for _ in range(2):
+        graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+        with torch.cuda.graph(graph):
+            outs.append(both(side))
+        graphs.append(graph)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(4):
+        for graph, st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                graph.replay()
+    torch.cuda.synchronize()
+    for out in outs:
+        assert all(torch.equal(a, b) for a, b in zip(out, want))
 
 
 def test_attn_decode_given_buffers():
