@@ -709,49 +709,82 @@ template <class C, int D> __global__ void __launch_bounds__(THREADS) k_attn(cons
     }
 }
 
-// The split segment that begins in run blockIdx.x: one head (blockIdx.y), its parts added in order.
+// The split segment that begins in run blockIdx.x: its head blockIdx.y, or (gridDim.y = 1) all of its
+// heads, their parts added in order, four parts' reads at a time.  A block's warps share a head's
+// parts; where a block has all heads and the parts are few, each warp takes heads of its own.
 template <typename E, int D> __global__ void __launch_bounds__(256) k_attn_join(const Args x) {
-    __shared__ float red[8][D], wm[8], wl[8];
+    constexpr int NC = D / 32, JW = 8, FEW = 8;
+    __shared__ float red[JW][D], wm[JW], wl[JW];
     after_previous();
     const int4 hd = x.head[blockIdx.x];
     if (hd.x < 0) return;
-    const int rb = hd.z & 0xffff, slot0 = hd.z >> 16, GB = x.GB, in = blockIdx.y, head = hd.y * x.G + rb * GB + in;
-    if (rb * GB + in >= x.G) return;
+    const int rb = hd.z & 0xffff, slot0 = hd.z >> 16, GB = x.GB, heads = min(GB, x.G - rb * GB);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n = hd.w - (int)blockIdx.x + 1;
-    constexpr int NC = D / 32;
-    auto part = [&](int i) {  // part i: the CTA's second slot only for a segment that begins behind another
-        return (size_t)(2 * (blockIdx.x + i) + (i == 0 ? slot0 : 0)) * GB + in;
-    };
-    float m = -CUDART_INF_F;
-    for (int i = threadIdx.x; i < n; i += 256) m = fmaxf(m, x.ml[part(i)].x);
-    m = warp_max(m);
-    if (lane == 0) wm[warp] = m;
-    __syncthreads();
-    for (int w = 0; w < 8; ++w) m = fmaxf(m, wm[w]);
-    float o[NC] = {}, l = 0.f;
-#pragma unroll 4
-    for (int i = warp; i < n; i += 8) {
-        const size_t at = part(i);
-        const float2 ml = x.ml[at];
-        const float *p = x.part + at * D;
-        const float f = ml.y == 0.f ? 0.f : ex2(ml.x - m);
-        l += ml.y * f;
+    const size_t row0 = (size_t)hd.x * x.a.Hq + hd.y * x.G + rb * GB;
+    const bool apart = n <= FEW && gridDim.y == 1 && GB > 1;
+    const int step = apart ? 1 : JW;
+    for (int in = apart ? warp : (int)blockIdx.y; in < heads; in += apart ? JW : (int)gridDim.y) {
+        float o[NC] = {}, m = -CUDART_INF_F, l = 0.f;
+        for (int i = apart ? 0 : warp; i < n; i += 4 * step) {
+            float2 ml[4];
+            float y[4][NC], mb = m;
 #pragma unroll
-        for (int c = 0; c < NC; ++c) o[c] += f * p[c * 32 + lane];
-    }
+            for (int u = 0; u < 4; ++u) {
+                const int k = i + u * step < n ? i + u * step : 0;  // behind the last part: the first one's, dropped
+                // a CTA's second slot only for a segment that begins behind another
+                const size_t at = (size_t)(2 * (blockIdx.x + k) + (k == 0 ? slot0 : 0)) * GB + in;
+                ml[u] = x.ml[at];
 #pragma unroll
-    for (int c = 0; c < NC; ++c) red[warp][c * 32 + lane] = o[c];
-    if (lane == 0) wl[warp] = l;
-    __syncthreads();
-    l = 0.f;
-    for (int w = 0; w < 8; ++w) l += wl[w];
-    const size_t row = (size_t)hd.x * x.a.Hq + head;
-    for (int c = threadIdx.x; c < D; c += 256) {
-        float s = 0.f;
-        for (int w = 0; w < 8; ++w) s += red[w][c];
-        ((E *)x.a.out)[row * D + c] = from_f<E>(l > 0.f ? s / l : (l == l ? 0.f : l));
+                for (int c = 0; c < NC; ++c) y[u][c] = x.part[at * D + c * 32 + lane];
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                if (i + u * step < n) mb = fmaxf(mb, ml[u].x);
+            const float g = m == mb ? 1.f : ex2(m - mb);  // equal: both may be -inf
+            m = mb;
+            l *= g;
+#pragma unroll
+            for (int c = 0; c < NC; ++c) o[c] *= g;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                if (i + u * step >= n) break;
+                const float f = ml[u].y == 0.f ? 0.f : ex2(ml[u].x - m);  // l = 0: the part's m may be -inf
+                l += ml[u].y * f;
+#pragma unroll
+                for (int c = 0; c < NC; ++c) o[c] += f * y[u][c];
+            }
+        }
+        const size_t row = row0 + in;
+        if (apart) {
+#pragma unroll
+            for (int c = 0; c < NC; ++c) ((E *)x.a.out)[row * D + c * 32 + lane] = from_f<E>(l > 0.f ? o[c] / l : (l == l ? 0.f : l));
+        } else {
+            __syncthreads();  // the head before is read
+#pragma unroll
+            for (int c = 0; c < NC; ++c) red[warp][c * 32 + lane] = o[c];
+            if (lane == 0) {
+                wm[warp] = m;
+                wl[warp] = l;
+            }
+            __syncthreads();
+            float g[JW];
+#pragma unroll
+            for (int w = 0; w < JW; ++w) m = fmaxf(m, wm[w]);
+            l = 0.f;
+#pragma unroll
+            for (int w = 0; w < JW; ++w) {
+                g[w] = wl[w] == 0.f ? 0.f : ex2(wm[w] - m);
+                l += wl[w] * g[w];
+            }
+            for (int c = threadIdx.x; c < D; c += JW * 32) {
+                float s = 0.f;
+#pragma unroll
+                for (int w = 0; w < JW; ++w) s += red[w][c] * g[w];
+                ((E *)x.a.out)[row * D + c] = from_f<E>(l > 0.f ? s / l : (l == l ? 0.f : l));
+            }
+        }
+        if (x.a.lse && lane == 0 && (apart || warp == 0)) x.a.lse[row] = lse_of(m, l);
     }
-    if (threadIdx.x == 0 && x.a.lse) x.a.lse[row] = lse_of(m, l);
     let_next();
 }
 
@@ -772,7 +805,13 @@ template <class C, int D> static cudaError_t launch(Args x, cudaStream_t s) {
     x.inv_ctas = 1.0 / ctas;
     e = launch_after(k_attn<C, D>, dim3(ctas), dim3(THREADS), smem, s, x);
     if (e != cudaSuccess) return e;
-    return launch_after(k_attn_join<typename C::E, D>, dim3(ctas, x.G < C::GB ? x.G : C::GB), dim3(256), 0, s, x);
+    // With few segments each may have many parts, and every head gets a block of its own; with more
+    // than an eighth of the CTAs there are a handful of parts on average, and one block takes a
+    // segment's heads, a warp each (200 requests of up to 2000 tokens: 41.4 us, with a block for every
+    // head of every run, most of them with nothing to do, 43.7; one request of 2000 tokens the other
+    // way round).
+    const bool many = (double)a.R * a.Hk * x.RB * 8 > MAX_CTAS;
+    return launch_after(k_attn_join<typename C::E, D>, dim3(ctas, many ? 1 : C::GB), dim3(256), 0, s, x);
 }
 
 static int heads_per_block(int G, bool bf16) {
