@@ -10,7 +10,7 @@
 //     page(p / page) * page + p % page (-1 where that page is -1)
 //
 // One launch, and what a CTA writes depends on no other CTA: every CTA forms both prefix sums over
-// all requests for itself in shared memory (64 KB at the most requests; 509 requests take about a
+// all requests for itself in shared memory (96 KB at the most requests; 509 requests take about a
 // microsecond), finds the request of a token or a page by bisection, and takes the page number of
 // a token from the table where the request had the page before and from the stack where it is
 // new.  So no CTA reads a table entry that another writes.  What bounds it is the launch and that
@@ -45,7 +45,7 @@ __device__ __forceinline__ int find(const int *sum, int lo, int hi, int x) {
 // UNROLL: tokens of a lane; a warp takes 32 UNROLL neighbouring tokens at a time
 template <int UNROLL> __global__ void __launch_bounds__(MAX_THREADS) k_pages(const Pages p) {
     extern __shared__ int sh[];
-    int *c = sh, *t = sh + p.R + 1;  // prefix sums [R + 1]: new tokens, new pages
+    int *c = sh, *t = c + p.R + 1, *had = t + p.R + 1;  // prefix sums [R + 1]: new tokens, new pages; cached tokens [R]
     __shared__ int wsum[2][MAX_THREADS / 32];
     const int threads = blockDim.x;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -55,6 +55,7 @@ template <int UNROLL> __global__ void __launch_bounds__(MAX_THREADS) k_pages(con
     int sc = 0, st = 0;
     for (int r = r0; r < r1; ++r) {
         const int a = max(p.cached[r], 0), f = max(p.fresh[r], 0);
+        had[r] = a;
         c[r] = f;
         t[r] = pages_of(add_sat(a, f), p) - pages_of(a, p);
         sc = add_sat(sc, c[r]);
@@ -105,19 +106,20 @@ template <int UNROLL> __global__ void __launch_bounds__(MAX_THREADS) k_pages(con
     auto page_of = [&](int nth) { return nth < free ? p.free_pages[free - 1 - nth] : -1; };
     for (unsigned r = gtid; r <= (unsigned)p.R; r += gsize) {
         p.cu_new[r] = c[r];
-        if (r < (unsigned)p.R) p.lens[r] = add_sat(max(p.cached[r], 0), max(p.fresh[r], 0));
+        if (r < (unsigned)p.R) p.lens[r] = add_sat(had[r], max(p.fresh[r], 0));
     }
     if (gtid == 0) *p.n_left = free - taken;
-    for (unsigned u = gtid; u < (unsigned)taken; u += gsize) {
+    // from the last thread down: where there are more warps than tokens' worth, those take the pages
+    for (unsigned u = gsize - 1 - gtid; u < (unsigned)taken; u += gsize) {
         const int i = (int)u, r = find(t, 0, p.R, i);
-        const int j = pages_of(max(p.cached[r], 0), p) + i - t[r];
+        const int j = pages_of(had[r], p) + i - t[r];
         p.table[(size_t)r * p.width + j] = page_of(i);
     }
     for (unsigned w = (gtid >> 5) * (32 * UNROLL); w < (unsigned)p.N; w += gsize * UNROLL) {
         int r[UNROLL], pos[UNROLL], pg[UNROLL];
         if (w < (unsigned)total) {  // the requests of the warp's first and last token, then the lanes' between them
             const int last = (int)min(w + (32 * UNROLL - 1), (unsigned)total - 1);
-            const int r0 = find(c, 0, p.R, (int)w), r1 = find(c, r0, p.R, last) + 1;
+            const int r0 = find(c, 0, p.R, (int)w), r1 = c[r0 + 1] > last ? r0 + 1 : find(c, r0, p.R, last) + 1;
 #pragma unroll
             for (int k = 0; k < UNROLL; ++k) r[k] = find(c, r0, r1, min((int)w + lane + 32 * k, last));
         }
@@ -127,7 +129,7 @@ template <int UNROLL> __global__ void __launch_bounds__(MAX_THREADS) k_pages(con
             pos[k] = 0;
             pg[k] = -1;
             if (n < (unsigned)total && n < (unsigned)p.N) {
-                const int a = max(p.cached[r[k]], 0);
+                const int a = had[r[k]];
                 pos[k] = add_sat(a, (int)n - c[r[k]]);
                 const int j = p.by_page.div(pos[k]), have = pages_of(a, p);
                 if (j < p.width) pg[k] = j < have ? p.table[(size_t)r[k] * p.width + j] : page_of(t[r[k]] + j - have);
@@ -149,7 +151,7 @@ template <int UNROLL> __global__ void __launch_bounds__(MAX_THREADS) k_pages(con
 cudaError_t pages_run(const Pages &args, cudaStream_t s) {
     Pages p = args;
     p.by_page = FastDiv(p.page);
-    const size_t smem = 2 * ((size_t)p.R + 1) * sizeof(int);
+    const size_t smem = (3 * (size_t)p.R + 2) * sizeof(int);
     // One token a lane in CTAs of 256 threads while one wave of them holds all tokens (66 tokens of 64
     // requests: 3.6 us, four a lane 5.1), else eight a lane, whose reads overlap and whose search is
     // shared, in CTAs of 1024, so that the prefix sums are formed once an SM (10^6 tokens of 509
