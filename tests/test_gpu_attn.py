@@ -6,8 +6,8 @@ Tolerances, per element, from the arithmetic.  A rounding to type t is off by at
 finfo(t).eps / 2 of the value.  fp32 steps are counted in units of 2^-24 of the largest operand:
   norm and rotation: y takes a sum of d squares by pairs (each term's sum at most 8 + log2(32)
     roundings deep), a root, two products and a rotation of two terms whose angle's cosine and sine
-    are off by 2^-22 or less: 64 units of the row's largest |y| cover them; gradients the same with
-    the row's largest |dy w| / rms, times (1 + the largest |n|^2) for the projection's term.
+    are off by 2^-22 or less (for bf16 results 2^-20): 64 units of the row's largest |y| cover them;
+    gradients the same with the row's largest |dy w| / rms, times (1 + the largest |n|^2) for the projection's term.
   attention: a score's sum of d products is off by at most (d + 4) 2^-23 sum |q_c k_c| scale; the
     weights then by twice that, relatively, and the exponential's 2^-21; splitting p into two bf16
     numbers leaves 2^-16 of it; sums over n tokens, 16 a step, four warps and up to 296 runs, (n / 16
