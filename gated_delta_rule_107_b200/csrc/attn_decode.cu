@@ -839,6 +839,7 @@ size_t attn_decode_ws_bytes(int Hq, int Hk, int d, bool bf16) {
 cudaError_t attn_decode_run(const AttnDecode &p, bool bf16, cudaStream_t s) {
     ad::Args x = {};
     x.a = p;
+    if (p.n_pages == 0) x.a.width = 0;  // no page: nothing is seen, no address is formed
     x.G = p.Hq / p.Hk;
     x.scale2 = p.scale * ad::LOG2E;
     x.by_page = FastDiv(p.page);

@@ -200,6 +200,30 @@ def test_qkrope_many_tokens_and_defaults():
     _check_norm_bwd(dq2, dwq2, q, None, pos, f, dqo, False, "bf16", "dq alone")
 
 
+def test_qkrope_single_tokens_and_one_sided_calls():
+    """A decoding batch [B, 1, heads, d] sliced from its projections, and calls with queries or keys alone."""
+    q, k, v, (wq, wk), f, pos = _qk_case("bf16", 9, 1, 6, 2, 128, 128, seed=17)
+    assert not q.is_contiguous()
+    qo, ko = binding.delta_rule_qkrope(q, k, wq, wk, f, pos)
+    torch.cuda.synchronize()
+    _check_norm(qo, q, wq, pos, f, False, "bf16", "q_out")
+    _check_norm(ko, k, wk, pos, f, False, "bf16", "k_out")
+    none, ko2 = binding.delta_rule_qkrope(q[:, :, :0], k, wq, wk, f, pos)
+    q2, k2 = q[:, 0], k[:, 0]  # [N, heads, d]
+    qo3, ko3 = binding.delta_rule_qkrope(q2, k2, wq, wk, f, pos.flatten())
+    kc, vc = (torch.zeros(3, 4, 2, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    out = binding.delta_rule_qkrope_cache(q2[:, :0], k2, v[:, 0], wq, wk, f, pos.flatten(), torch.arange(9, device="cuda"), kc, vc)
+    torch.cuda.synchronize()
+    assert none.numel() == out.numel() == 0 and torch.equal(ko2, ko)
+    assert torch.equal(qo3, qo[:, 0]) and torch.equal(ko3, ko[:, 0])
+    assert torch.equal(kc.view(12, 2, 128)[:9], ko[:, 0]) and torch.equal(vc.view(12, 2, 128)[:9], v[:, 0])
+    e = q[:0]
+    empty = binding.delta_rule_qkrope(e, k[:0], wq, wk, f, pos[:0])
+    g = binding.delta_rule_qkrope_bwd(e, k[:0], wq, wk, f, empty[0], empty[1], pos[:0])
+    torch.cuda.synchronize()
+    assert empty[0].shape == e.shape and (g[2] == 0).all() and (g[3] == 0).all()  # sums over no rows
+
+
 def test_qkrope_far_positions_keep_their_angle():
     """At positions of 10^6 and 2^31 - 1 the angles are as exact as at small ones."""
     for far in (1000000, 2 ** 31 - 6000):
@@ -375,6 +399,47 @@ def test_attn_decode_splits(dtype, lens, Hq, Hk):
     for _ in range(3):  # the split is joined in order: bit for bit
         o2, l2 = binding.delta_rule_attn_decode(q, kc, vc, table, _i32(lens), want_lse=True)
         assert torch.equal(o, o2) and torch.equal(lse, l2)
+
+
+@pytest.mark.parametrize("dtype", ("f32", "bf16"))
+def test_attn_decode_many_requests(dtype):
+    """More requests than threads of a block, most of them of a tile or less: several share every block."""
+    lens = [(7 * i) % 23 for i in range(777)]
+    lens[400] = 1500
+    kc, vc, table = _cache(dtype, lens, 8, 1, 64, seed=41)
+    q = _randn(_rng(9), 777, 2, 64, dtype=dtype, scale=2.0)
+    o, lse = binding.delta_rule_attn_decode(q, kc, vc, table, _i32(lens), want_lse=True)
+    torch.cuda.synchronize()
+    _check_attn(o, lse, q, kc, vc, table, lens, dtype)
+
+
+@pytest.mark.parametrize("dtype", ("f32", "bf16"))
+@pytest.mark.parametrize("page", (5, 32))
+def test_attn_decode_caches_of_different_strides(dtype, page):
+    lens = [100, 3, 64]
+    kc, vc, table = _cache(dtype, lens, page, 2, 128, seed=page)
+    P = kc.shape[0]
+    kb = torch.full((P, 2, *kc.shape[1:]), float("nan"), dtype=DT[dtype], device="cuda")
+    vb = torch.full((P, 3, *kc.shape[1:]), float("nan"), dtype=DT[dtype], device="cuda")
+    kb[:, 1], vb[:, 2] = kc, vc
+    q = _randn(_rng(9), 3, 10, 128, dtype=dtype)
+    want = binding.delta_rule_attn_decode(q, kc, vc, table, _i32(lens), want_lse=True)
+    got = binding.delta_rule_attn_decode(q, kb[:, 1], vb[:, 2], table, _i32(lens), want_lse=True)
+    torch.cuda.synchronize()
+    _check_attn(*want, q, kc, vc, table, lens, dtype)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_attn_decode_without_pages_or_table():
+    q = _randn(_rng(9), 3, 4, 64, dtype="bf16")
+    none = torch.empty(0, 16, 2, 64, dtype=torch.bfloat16, device="cuda")
+    kc = torch.zeros(2, 16, 2, 64, dtype=torch.bfloat16, device="cuda")
+    for cache, table in ((none, _i32([[0, 1]] * 3)), (kc, torch.empty(3, 0, dtype=torch.int32, device="cuda"))):
+        o, lse = binding.delta_rule_attn_decode(q, cache, cache, table, _i32([5, 0, 40]), want_lse=True)
+        torch.cuda.synchronize()
+        assert (o == 0).all() and torch.isneginf(lse).all()
+    o, lse = binding.delta_rule_attn_decode(q[:0], kc, kc, _i32([[0]])[:0], _i32([0])[:0], want_lse=True)
+    assert o.shape == (0, 4, 64) and lse.shape == (0, 4)
 
 
 @pytest.mark.parametrize("dtype", ("f32", "bf16"))
