@@ -288,8 +288,7 @@ template <typename E, int D, int TILE_, int STAGES> struct Pipe {
 
 // ------------------------------------------------------------------ one warp's arithmetic
 // Each keeps, for the heads of a block, m (base 2), l and o, and offers
-//   fetch(q row of the block's first head, heads): reads the queries; share(place in shared memory),
-//     where warps share them; begin(): they are the ones from now
+//   fetch(q row of the block's first head, heads): reads the queries; begin(): they are the ones from now
 //   tile(stage, live)
 //   finish(m, l, o): l summed over lanes, all three to shared memory, o as [head][slot_of(head, channel)]
 
@@ -432,7 +431,6 @@ template <int D, int NT> struct Mma {  // bf16: blocks of 8 NT heads
             }
         }
     }
-    __device__ __forceinline__ void share(float *) {}
     __device__ __forceinline__ void finish(float *sm, float *sl, float *so) {
         const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
 #pragma unroll
@@ -453,81 +451,118 @@ template <int D, int NT> struct Mma {  // bf16: blocks of 8 NT heads
                 }
             }
     }
-    static constexpr int EXTRA = 0, SHARED = 0;  // bytes of shared memory: of the warp's own, of the CTA's warps together
+    static constexpr int EXTRA = 0;  // bytes of shared memory of the warp's own
 };
 
-template <int D, int H> struct Simt {  // fp32: blocks of H heads, at most 8
+// The N values of 2 MASK neighbouring lanes added up, each lane keeping max(1, N / (2 MASK)) of the sums
+// in v[0], v[1], ...: its highest bit names the half, the next one the half of that, and so on; once a
+// single sum is left, the lanes of the remaining bits all keep it.
+template <int N, int MASK> __device__ __forceinline__ void scatter_sums(float *v) {
+    if constexpr (MASK > 0) {
+        constexpr int HALF = N > 1 ? N / 2 : 1;
+#pragma unroll
+        for (int i = 0; i < HALF; ++i) {
+            if constexpr (N > 1) {
+                const bool up = threadIdx.x & MASK;
+                const float send = up ? v[i] : v[i + HALF], keep = up ? v[i + HALF] : v[i];
+                v[i] = keep + __shfl_xor_sync(0xffffffffu, send, MASK);
+            } else {
+                v[i] += __shfl_xor_sync(0xffffffffu, v[i], MASK);
+            }
+        }
+        scatter_sums<HALF, MASK / 2>(v);
+    }
+}
+
+// fp32: blocks of H heads, at most 8.  A lane holds 4 channels of the block's queries in registers and
+// forms its part of the scores of 8 rows (its half-warp's rows where a row has 16 chunks); the parts
+// are added so that each lane ends with the scores of one token and C heads.  (With the queries in
+// shared memory, every lane of a token reading all of them, blocks of 8 heads were bound by shared
+// memory: 113 us instead of XX for 32 requests of 1525 tokens, 64 / 8 heads of 128 channels.)
+template <int D, int H> struct Simt {
     typedef float E;
     static constexpr int GB = H, STAGES = 3, CTAS = MAX_CTAS, NC = D / 32, TILE = 1024 / D;
     typedef Pipe<E, D, TILE, STAGES> P;
-    f2 o[GB][NC / 2];
-    float m[GB], l[GB], qn[GB * D / THREADS > 0 ? GB * D / THREADS : 1];
-    static constexpr int EXTRA = TILE * GB * 8;  // the tile's p, each twice (one packed operand)
-    static constexpr int SHARED = GB * D * 4;    // the block's queries
+    static constexpr int LR = D / 4, TP = 32 / LR;         // lanes of a row, rows side by side
+    static constexpr int LT = LR / 8;                      // lanes of a token, once the scores are added
+    static constexpr int HG = H < LT ? H : LT, C = H / HG;  // groups of heads, heads of a lane
+    f2 o[GB][NC / 2], q[GB][2], qn[GB][2];
+    float m[C], l[C];
+    // the tile's p and the heads' factors, each twice (one packed operand); the next warp's stages behind
+    // it stay aligned
+    static constexpr int EXTRA = ((TILE + 1) * GB * 8 + 127) / 128 * 128;
     f2 *ps;
-    const float *qs;
 
-    // the queries are read by all threads together, and shared by the warps
+    // the lane's token of a tile, its first head, and whether it is the first of lanes with the same
+    static __device__ __forceinline__ int token() { return (threadIdx.x % LR / LT) * TP + (threadIdx.x & 31) / LR; }
+    static __device__ __forceinline__ int head() { return threadIdx.x % LT / (LT / HG) * C; }
+    static __device__ __forceinline__ bool first() { return threadIdx.x % LT % (LT / HG) == 0; }
+
     __device__ __forceinline__ void fetch(const E *src, int heads) {
+        const int c = threadIdx.x % LR;
 #pragma unroll
-        for (int i = 0; i < (GB * D + THREADS - 1) / THREADS; ++i) {
-            const int at = i * THREADS + threadIdx.x;
-            qn[i] = at < heads * D ? src[at] : 0.f;
+        for (int h = 0; h < GB; ++h) {
+            const float4 x = h < heads ? *reinterpret_cast<const float4 *>(src + h * D + 4 * c) : make_float4(0.f, 0.f, 0.f, 0.f);
+            qn[h][0] = mk(x.x, x.y);
+            qn[h][1] = mk(x.z, x.w);
         }
-    }
-    __device__ __forceinline__ void share(float *to) {
-#pragma unroll
-        for (int i = 0; i < (GB * D + THREADS - 1) / THREADS; ++i) {
-            const int at = i * THREADS + threadIdx.x;
-            if (at < GB * D) to[at] = qn[i];
-        }
-        qs = to;
     }
     __device__ __forceinline__ void begin() {
 #pragma unroll
+        for (int c = 0; c < C; ++c) {
+            m[c] = -CUDART_INF_F;
+            l[c] = 0.f;
+        }
+#pragma unroll
         for (int h = 0; h < GB; ++h) {
-            m[h] = -CUDART_INF_F;
-            l[h] = 0.f;
+            q[h][0] = qn[h][0];
+            q[h][1] = qn[h][1];
 #pragma unroll
             for (int c = 0; c < NC / 2; ++c) o[h][c] = 0;
         }
     }
     __device__ __forceinline__ void tile(uint32_t, uint32_t live, float scale2, const char *base) {
-        const int lane = threadIdx.x & 31, t = lane & (TILE - 1), part = lane / TILE;
-        f2 s2[GB] = {};
-#pragma unroll 4
-        for (int c = 0; c < 8; ++c) {  // the lane's 32 channels
-            const int ch = part * 8 + c;
-            const float4 k = *reinterpret_cast<const float4 *>(base + P::at(t, ch));
+        const int lane = threadIdx.x & 31;
+        float s[8 * GB];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float4 k = *reinterpret_cast<const float4 *>(base + P::at(i * TP + lane / LR, lane % LR));
             const f2 k0 = mk(k.x, k.y), k1 = mk(k.z, k.w);
 #pragma unroll
-            for (int h = 0; h < GB; ++h) {
-                const float4 q = *reinterpret_cast<const float4 *>(qs + h * D + 4 * ch);
-                s2[h] = fma(k0, mk(q.x, q.y), s2[h]);
-                s2[h] = fma(k1, mk(q.z, q.w), s2[h]);
+            for (int h = 0; h < GB; ++h) s[i * GB + h] = sum2(fma(k1, q[h][1], mul(k0, q[h][0])));
+        }
+        scatter_sums<8 * GB, LR / 2>(s);
+        const int t = token(), h0 = head();
+        const bool ok = live >> t & 1;
+        float mx[C];
+#pragma unroll
+        for (int c = 0; c < C; ++c) mx[c] = s[c] = ok ? s[c] * scale2 : -CUDART_INF_F;
+#pragma unroll
+        for (int d = LT; d < 32; d <<= 1)
+#pragma unroll
+            for (int c = 0; c < C; ++c) mx[c] = fmaxf(mx[c], __shfl_xor_sync(0xffffffffu, mx[c], d));
+        bool up = false;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const float mn = fmaxf(m[c], mx[c]);
+            const float f = m[c] == mn ? 1.f : ex2(m[c] - mn);  // equal: both may be -inf
+            up = up || m[c] != mn;
+            m[c] = mn;
+            const float p = s[c] == -CUDART_INF_F ? 0.f : ex2(s[c] - mn);  // -inf minus -inf must not be NaN
+            l[c] = l[c] * f + p;
+            if (first()) {
+                ps[t * GB + h0 + c] = mk(p, p);
+                if (t == 0) ps[TILE * GB + h0 + c] = mk(f, f);
             }
         }
-        const bool ok = live >> t & 1;
-#pragma unroll
-        for (int h = 0; h < GB; ++h) {
-            float s = sum2(s2[h]);
-#pragma unroll
-            for (int d = TILE; d < 32; d <<= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-            s = ok ? s * scale2 : -CUDART_INF_F;
-            float mx = s;
-#pragma unroll
-            for (int d = 1; d < TILE; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-            const float mn = fmaxf(m[h], mx);
-            const float f = m[h] == mn ? 1.f : ex2(m[h] - mn);
-            m[h] = mn;
-            const float p = s == -CUDART_INF_F ? 0.f : ex2(s - mn);
-            l[h] = l[h] * f + (part == 0 ? p : 0.f);  // each token counts once over the warp
-            if (part == 0) ps[t * GB + h] = mk(p, p);
-            const f2 ff = mk(f, f);
-#pragma unroll
-            for (int c = 0; c < NC / 2; ++c) o[h][c] = mul(o[h][c], ff);
-        }
+        up = __any_sync(0xffffffffu, up);
         __syncwarp();
+        if (up) {
+#pragma unroll
+            for (int h = 0; h < GB; ++h)
+#pragma unroll
+                for (int c = 0; c < NC / 2; ++c) o[h][c] = mul(o[h][c], ps[TILE * GB + h]);
+        }
         const char *v = base + P::HALF;
 #pragma unroll 4
         for (int u = 0; u < TILE; ++u) {
@@ -553,20 +588,23 @@ template <int D, int H> struct Simt {  // fp32: blocks of H heads, at most 8
     __device__ __forceinline__ void finish(float *sm, float *sl, float *so) {
         const int lane = threadIdx.x & 31;
 #pragma unroll
-        for (int h = 0; h < GB; ++h) {
-            l[h] = warp_sum(l[h]);
-            if (lane == 0) {
-                sm[h] = m[h];
-                sl[h] = l[h];
+        for (int c = 0; c < C; ++c) {
+#pragma unroll
+            for (int d = LT; d < 32; d <<= 1) l[c] += __shfl_xor_sync(0xffffffffu, l[c], d);
+            if (first() && token() == 0) {
+                sm[head() + c] = m[c];
+                sl[head() + c] = l[c];
             }
+        }
+#pragma unroll
+        for (int h = 0; h < GB; ++h)
 #pragma unroll
             for (int c = 0; c < NC / 2; ++c) *reinterpret_cast<f2 *>(so + h * D + slot_of(h, lane * NC + 2 * c)) = o[h][c];
-        }
     }
 };
 
 template <class C, int D> constexpr int warp_bytes() { return C::STAGES * C::P::STAGE + C::EXTRA; }
-template <class C, int D> constexpr int smem_bytes() { return WARPS * warp_bytes<C, D>() + C::SHARED; }
+template <class C, int D> constexpr int smem_bytes() { return WARPS * warp_bytes<C, D>(); }
 
 template <class C, int D> __global__ void __launch_bounds__(THREADS) k_attn(const Args x) {
     typedef typename C::E E;
@@ -576,6 +614,7 @@ template <class C, int D> __global__ void __launch_bounds__(THREADS) k_attn(cons
     __shared__ float sm_m[WARPS][GB], sm_l[WARPS][GB];
     __shared__ int sm_at[WARPS];
     static_assert(GB * D * 4 <= P::STAGE, "a warp's o fits a stage");
+    static_assert(warp_bytes<C, D>() % 128 == 0, "every warp's stages are aligned");
     const AttnDecode &a = x.a;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int segs = a.Hk * x.RB;
@@ -637,15 +676,12 @@ template <class C, int D> __global__ void __launch_bounds__(THREADS) k_attn(cons
 
     C c;
     if constexpr (C::EXTRA > 0) c.ps = reinterpret_cast<f2 *>(mine + STAGES * P::STAGE);
-    float *together = reinterpret_cast<float *>(smem + WARPS * warp_bytes<C, D>());
     int done = 0, mytile = warp;  // the run's tiles before the current segment; the warp's next one
     auto fetch = [&](const Place &pl) {
         const int h = pl.seg / x.RB, rb = pl.seg - h * x.RB;
         c.fetch((const E *)a.q + ((size_t)pl.r * a.Hq + h * x.G + rb * GB) * D, min(GB, x.G - rb * GB));
     };
     fetch(here);
-    c.share(together);
-    if (C::SHARED > 0) __syncthreads();
     for (int part = 0; here.unit < run.len; ++part) {
         const int h = here.seg / x.RB, rb = here.seg - h * x.RB, head0 = h * x.G + rb * GB;
         const int heads = min(GB, x.G - rb * GB);
@@ -672,7 +708,6 @@ template <class C, int D> __global__ void __launch_bounds__(THREADS) k_attn(cons
         c.finish(sm_m[warp], sm_l[warp], reinterpret_cast<float *>(mine + put * P::STAGE));
         if (lane == 0) sm_at[warp] = warp * warp_bytes<C, D>() + put * P::STAGE;
         __syncthreads();  // all warps are done with the segment
-        c.share(together);
         const size_t slot = 2 * blockIdx.x + (part > 0);
         for (int i = tid; i < heads * (D / 8); i += THREADS) {
             const int hd = i / (D / 8), ch = (i - hd * (D / 8)) * 8;
