@@ -33,9 +33,9 @@
 //     into two bf16 numbers (high and rest, 2^-17 of p) and multiplied twice: rounding P once
 //     would put as large an error in the output as its own rounding, and the second product is
 //     hidden behind the loads.  Groups of 16 reach 83 to 90 % of the copy's rate, of 32 45 %.
-//   fp32.  CUDA cores, 1, 2, 4 or up to 8 heads at a time, packed arithmetic: a lane holds 32
-//     channels of one token for the scores, 1/32 of the channels of every head for the output.  Groups
-//     of up to 4 are bound by the loads (81 to 92 % of the copy's rate), of 8 by shared memory's (57 %).
+//   fp32.  CUDA cores, 1, 2, 4 or up to 8 heads at a time, packed arithmetic: a lane holds 4 channels
+//     of the heads' queries and outputs.  Groups of up to 4 are bound by the loads (87 to 94 % of the
+//     copy's rate), of 8 by two warps a scheduler working through their tiles (68 to 70 %).
 // Tokens that are masked (or whose table entry is no page) are neither read nor seen: their rows
 // in shared memory are zero-filled, their scores -inf.  A request with none gives o = 0, lse = -inf.
 #include <math_constants.h>
@@ -478,15 +478,15 @@ template <int N, int MASK> __device__ __forceinline__ void scatter_sums(float *v
 // forms its part of the scores of 8 rows (its half-warp's rows where a row has 16 chunks); the parts
 // are added so that each lane ends with the scores of one token and C heads.  (With the queries in
 // shared memory, every lane of a token reading all of them, blocks of 8 heads were bound by shared
-// memory: 113 us instead of XX for 32 requests of 1525 tokens, 64 / 8 heads of 128 channels.)
+// memory: 113 us instead of 89 for 32 requests of 1525 tokens, 64 / 8 heads of 128 channels.)
 template <int D, int H> struct Simt {
     typedef float E;
-    static constexpr int GB = H, STAGES = 3, CTAS = MAX_CTAS, NC = D / 32, TILE = 1024 / D;
+    static constexpr int GB = H, STAGES = 3, CTAS = MAX_CTAS, TILE = 1024 / D;
     typedef Pipe<E, D, TILE, STAGES> P;
     static constexpr int LR = D / 4, TP = 32 / LR;         // lanes of a row, rows side by side
     static constexpr int LT = LR / 8;                      // lanes of a token, once the scores are added
     static constexpr int HG = H < LT ? H : LT, C = H / HG;  // groups of heads, heads of a lane
-    f2 o[GB][NC / 2], q[GB][2], qn[GB][2];
+    f2 o[GB][2], q[GB][2], qn[GB][2];
     float m[C], l[C];
     // the tile's p and the heads' factors, each twice (one packed operand); the next warp's stages behind
     // it stay aligned
@@ -518,7 +518,7 @@ template <int D, int H> struct Simt {
             q[h][0] = qn[h][0];
             q[h][1] = qn[h][1];
 #pragma unroll
-            for (int c = 0; c < NC / 2; ++c) o[h][c] = 0;
+            for (int c = 0; c < 2; ++c) o[h][c] = 0;
         }
     }
     __device__ __forceinline__ void tile(uint32_t, uint32_t live, float scale2, const char *base) {
@@ -561,26 +561,26 @@ template <int D, int H> struct Simt {
 #pragma unroll
             for (int h = 0; h < GB; ++h)
 #pragma unroll
-                for (int c = 0; c < NC / 2; ++c) o[h][c] = mul(o[h][c], ps[TILE * GB + h]);
+                for (int c = 0; c < 2; ++c) o[h][c] = mul(o[h][c], ps[TILE * GB + h]);
         }
         const char *v = base + P::HALF;
 #pragma unroll 4
-        for (int u = 0; u < TILE; ++u) {
-            f2 x[NC / 2];
-            const char *at = v + P::at(u, lane * NC / 4) + (lane * NC % 4) * 4;
-            if constexpr (NC == 4) {
-                const float4 y = *reinterpret_cast<const float4 *>(at);
-                x[0] = mk(y.x, y.y);
-                x[1] = mk(y.z, y.w);
+        for (int i = 0; i < 8; ++i) {
+            const int u = i * TP + lane / LR;
+            const float4 y = *reinterpret_cast<const float4 *>(v + P::at(u, lane % LR));
+            const f2 x0 = mk(y.x, y.y), x1 = mk(y.z, y.w);
+            if constexpr (GB == 1) {
+                o[0][0] = fma(ps[u], x0, o[0][0]);
+                o[0][1] = fma(ps[u], x1, o[0][1]);
             } else {
-                const float2 y = *reinterpret_cast<const float2 *>(at);
-                x[0] = mk(y.x, y.y);
-            }
 #pragma unroll
-            for (int h = 0; h < GB; ++h) {
-                const f2 p = ps[u * GB + h];
-#pragma unroll
-                for (int c = 0; c < NC / 2; ++c) o[h][c] = fma(p, x[c], o[h][c]);
+                for (int h = 0; h < GB; h += 2) {
+                    const ulonglong2 p = *reinterpret_cast<const ulonglong2 *>(ps + u * GB + h);
+                    o[h][0] = fma(p.x, x0, o[h][0]);
+                    o[h][1] = fma(p.x, x1, o[h][1]);
+                    o[h + 1][0] = fma(p.y, x0, o[h + 1][0]);
+                    o[h + 1][1] = fma(p.y, x1, o[h + 1][1]);
+                }
             }
         }
         __syncwarp();  // ps is free for the next tile
@@ -597,9 +597,16 @@ template <int D, int H> struct Simt {
             }
         }
 #pragma unroll
-        for (int h = 0; h < GB; ++h)
+        for (int h = 0; h < GB; ++h) {
+            float x[4];
+            un(o[h][0], x[0], x[1]);
+            un(o[h][1], x[2], x[3]);
 #pragma unroll
-            for (int c = 0; c < NC / 2; ++c) *reinterpret_cast<f2 *>(so + h * D + slot_of(h, lane * NC + 2 * c)) = o[h][c];
+            for (int d = LR; d < 32; d <<= 1)  // the rows side by side
+#pragma unroll
+                for (int c = 0; c < 4; ++c) x[c] += __shfl_xor_sync(0xffffffffu, x[c], d);
+            if (lane < LR) *reinterpret_cast<float4 *>(so + h * D + slot_of(h, 4 * lane)) = make_float4(x[0], x[1], x[2], x[3]);
+        }
     }
 };
 
