@@ -127,6 +127,32 @@ at::Tensor empty(at::IntArrayRef shape, at::ScalarType type, at::Device dev) {
 }
 at::Tensor like(const at::Tensor &t) { return empty(t.sizes(), t.scalar_type(), t.device()); }
 
+// Several new dense tensors side by side in one allocation, each beginning at a multiple of its element
+// size (an allocation takes half a microsecond).  All of it lives as long as any of them, so outputs
+// beyond a megabyte get allocations of their own.
+struct Together {
+    at::Tensor all;
+    int64_t at = 0;
+    Together(int64_t bytes, at::Device dev) : all(empty({bytes}, at::kByte, dev)) {}
+    at::Tensor next(at::ScalarType type, at::IntArrayRef shape) {
+        const int64_t size = (int64_t)c10::elementSize(type);
+        auto t = c10::make_intrusive<c10::TensorImpl>(c10::Storage(all.storage()), all.key_set(), c10::scalarTypeToTypeMeta(type));
+        t->set_storage_offset(at / size);
+        t->set_sizes_contiguous(shape);
+        at += t->numel() * size;
+        return at::Tensor(std::move(t));
+    }
+};
+constexpr int64_t SMALL = 1 << 20;
+// two tensors like a and b
+std::pair<at::Tensor, at::Tensor> like_both(const at::Tensor &a, const at::Tensor &b) {
+    const int64_t bytes = (a.numel() + b.numel()) * a.element_size();
+    if (bytes > SMALL || a.numel() * a.element_size() % 256) return {like(a), like(b)};
+    Together t(bytes, a.device());
+    at::Tensor x = t.next(a.scalar_type(), a.sizes());
+    return {x, t.next(b.scalar_type(), b.sizes())};
+}
+
 PyObject *code(int rc) { return PyLong_FromLong(rc); }
 template <typename... T> PyObject *give(const T &...t) {
     PyObject *r = PyTuple_New(sizeof...(t));
@@ -161,19 +187,9 @@ PyObject *pages(PyObject *, Args a, Py_ssize_t n) {
          *sp = dense(stack, "free_pages", at::kInt, dev, -1), *np = dense(n_free, "n_free", at::kInt, dev, 1),
          *tp = dense(table, "table", at::kInt, dev, -1);
     On on(dev);
-    // the five outputs side by side in one allocation (five take 2 us more), the 8-byte ones first
-    const at::Tensor all = empty({12ll * N + 8ll * R + 8}, at::kByte, dev);
-    int64_t at = 0;
-    auto next = [&](at::ScalarType type, int64_t n) {
-        auto t = c10::make_intrusive<c10::TensorImpl>(c10::Storage(all.storage()), all.key_set(), c10::scalarTypeToTypeMeta(type));
-        const int64_t size = (int64_t)c10::elementSize(type);
-        t->set_storage_offset(all.storage_offset() + at / size);
-        t->set_sizes_contiguous(n);
-        at += n * size;
-        return at::Tensor(std::move(t));
-    };
-    const at::Tensor slots = next(at::kLong, N), pos = next(at::kInt, N), lens = next(at::kInt, R), cu = next(at::kInt, R + 1ll),
-                     left = next(at::kInt, 1);
+    Together t(12ll * N + 8ll * R + 8, dev);  // the 8-byte elements first
+    const at::Tensor slots = t.next(at::kLong, {N}), pos = t.next(at::kInt, {N}), lens = t.next(at::kInt, {R}),
+                     cu = t.next(at::kInt, {R + 1ll}), left = t.next(at::kInt, {1});
     const int rc = c_pages((int *)cp, (int *)fp, (int *)sp, (int *)np, (int *)tp, (int *)lens.data_ptr(), (int *)cu.data_ptr(),
                            (int *)pos.data_ptr(), (long long *)slots.data_ptr(), (int *)left.data_ptr(), R,
                            extent(stack.numel(), "free_pages"), extent(table.size(1), "table"), page, N, on.stream);
@@ -219,7 +235,7 @@ PyObject *qkrope(PyObject *, Args a, Py_ssize_t n) {
     const QK x(a);
     const bool inter = truth(a[6]);
     On on(x.dev);
-    at::Tensor qo = like(x.q), ko = like(x.k);
+    const auto [qo, ko] = like_both(x.q, x.k);
     const int rc = c_qkrope(x.q.data_ptr(), x.k.data_ptr(), x.wq, x.wk, x.f, x.pos, qo.data_ptr(), ko.data_ptr(), x.B, x.T, x.Hq,
                             x.Hk, x.d, x.rot, inter, x.qs, x.ks, x.dtype, on.stream);
     return rc == DR_OK ? give(qo, ko) : code(rc);
@@ -246,15 +262,18 @@ PyObject *qkrope_bwd(PyObject *, Args a, Py_ssize_t n) {
     same_shape(gk, "dk_out", x.k.sizes());
     void *gqp = dense(gq, "dq_out", x.q.scalar_type(), x.dev, -1), *gkp = dense(gk, "dk_out", x.q.scalar_type(), x.dev, -1);
     On on(x.dev);
-    const at::Tensor dq = out_like(a[9], "dq", x.q), dk = out_like(a[10], "dk", x.k);
+    const bool ours = a[9] == Py_None && a[10] == Py_None;
+    const auto [nq, nk] = ours ? like_both(x.q, x.k) : std::pair(out_like(a[9], "dq", x.q), out_like(a[10], "dk", x.k));
+    const at::Tensor &dq = nq, &dk = nk;
     const long long dqs = token_stride(dq, "dq"), dks = token_stride(dk, "dk");
     at::Tensor dwq, dwk, ws;
     size_t need = 0;
     if (want) {
         need = c_qkrope_ws(x.d);
         if (need == (size_t)-1) return code(DR_ERR_UNSUPPORTED);
-        dwq = empty({x.d}, at::kFloat, x.dev);
-        dwk = empty({x.d}, at::kFloat, x.dev);
+        Together t(8ll * x.d, x.dev);
+        dwq = t.next(at::kFloat, {x.d});
+        dwk = t.next(at::kFloat, {x.d});
         ws = empty({(int64_t)need}, at::kByte, x.dev);
     }
     const int rc = c_qkrope_bwd(x.q.data_ptr(), x.k.data_ptr(), x.wq, x.wk, x.f, x.pos, gqp, gkp, dq.data_ptr(), dk.data_ptr(),
@@ -325,10 +344,17 @@ PyObject *attn_decode(PyObject *, Args a, Py_ssize_t n) {
     const size_t need = c_attn_ws(Hq, Hk, d, dtype);
     if (need == (size_t)-1) return code(Hq > 0 && Hk > 0 && Hq % Hk == 0 && d > 0 ? DR_ERR_UNSUPPORTED : DR_ERR_ARG);
     On on(dev);
-    const at::Tensor out = out_like(a[8], "out", q);
-    TORCH_CHECK_VALUE(out.is_contiguous(), "out must be contiguous");
-    at::Tensor lse, ws;
-    if (want) lse = empty({R, Hq}, at::kFloat, dev);
+    at::Tensor out, lse, ws;
+    const int64_t bytes = q.numel() * q.element_size();
+    if (want && a[8] == Py_None && bytes <= SMALL && bytes % 256 == 0) {
+        Together t(bytes + 4ll * R * Hq, dev);
+        out = t.next(q.scalar_type(), q.sizes());
+        lse = t.next(at::kFloat, {R, Hq});
+    } else {
+        out = out_like(a[8], "out", q);
+        TORCH_CHECK_VALUE(out.is_contiguous(), "out must be contiguous");
+        if (want) lse = empty({R, Hq}, at::kFloat, dev);
+    }
     if (a[9] != Py_None) {
         ws = tensor(a[9], "workspace");
         dense(ws, "workspace", at::kByte, dev, -1);
