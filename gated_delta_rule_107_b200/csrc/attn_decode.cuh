@@ -1,6 +1,6 @@
 // attn_decode.cuh -- attention of one new token over a paged key-value cache (attn_decode.cu).
 #pragma once
-#include "dr_common.cuh"
+#include "softmax_layer.cuh"
 
 namespace dr {
 

@@ -1,6 +1,6 @@
 // pages.cuh -- pages of a key-value cache given to requests (pages.cu).
 #pragma once
-#include "dr_common.cuh"
+#include "softmax_layer.cuh"
 
 namespace dr {
 

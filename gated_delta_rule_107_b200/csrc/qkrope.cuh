@@ -1,6 +1,6 @@
 // qkrope.cuh -- norm of query and key heads with the rotation by position (qkrope.cu).
 #pragma once
-#include "dr_common.cuh"
+#include "softmax_layer.cuh"
 
 namespace dr {
 
