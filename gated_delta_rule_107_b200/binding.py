@@ -143,11 +143,11 @@ def load(path: str | None = None):
     lib.delta_rule_qkrope_workspace_size.restype = sz
     lib.delta_rule_qkrope_bwd.argtypes = [vp] * 12 + [i] * 7 + [ll] * 4 + [i, vp, sz, vp]
     lib.delta_rule_qkrope_bwd.restype = i
-    lib.delta_rule_qkrope_cache.argtypes = [vp] * 11 + [i] * 6 + [ll] * 3 + [i] * 2 + [ll] * 2 + [i, vp]
+    lib.delta_rule_qkrope_cache.argtypes = [vp] * 11 + [i] * 6 + [ll] * 3 + [i] * 2 + [ll] * 6 + [i, vp]
     lib.delta_rule_qkrope_cache.restype = i
     lib.delta_rule_attn_decode_workspace_size.argtypes = [i] * 4
     lib.delta_rule_attn_decode_workspace_size.restype = sz
-    lib.delta_rule_attn_decode.argtypes = [vp] * 7 + [i] * 7 + [ll] * 2 + [ctypes.c_float, i, i, vp, sz, vp]
+    lib.delta_rule_attn_decode.argtypes = [vp] * 7 + [i] * 7 + [ll] * 6 + [ctypes.c_float, i, i, vp, sz, vp]
     lib.delta_rule_attn_decode.restype = i
     if path is None:
         _lib = lib
@@ -669,7 +669,8 @@ def delta_rule_qkrope_bwd(q, k, wq, wk, inv_freq, dq_out, dk_out, positions=None
 def delta_rule_qkrope_cache(q, k, v, wq, wk, inv_freq, positions, slots, k_cache, v_cache, interleaved=False,
                             q_out=None):
     """delta_rule_qkrope for serving: returns q_out; the keys (normed, rotated) and the values go into rows
-    slots (int64, one a token; negative: padding, not written) of the caches [pages, page, Hk, d]."""
+    slots (int64, one a token; negative: padding, not written) of the caches [pages, page, Hk, d], of any
+    strides with dense channels."""
     return _given(_calls().qkrope_cache(q, k, wq, wk, inv_freq, positions, interleaved, v, slots, k_cache, v_cache,
                                         q_out), "delta_rule_qkrope_cache")[0]
 
@@ -678,7 +679,7 @@ def delta_rule_attn_decode(q, k_cache, v_cache, table, lens, scale=None, window=
                            workspace: torch.Tensor | None = None):
     """Attention of one new token per request over the paged cache: (out, lse or None).
 
-    q [R, Hq, d]; caches [pages, page, Hk, d]; table int32 [R, width]; lens int32 [R], cached tokens, the
+    q [R, Hq, d]; caches [pages, page, Hk, d] of any strides with dense channels; table int32 [R, width]; lens int32 [R], cached tokens, the
     new one among them; scale: of the scores (None: d ** -0.5); window: the last tokens seen (0: all)."""
     return _given(_calls().attn_decode(q, k_cache, v_cache, table, lens, scale, window, want_lse, out, workspace),
                   "delta_rule_attn_decode")

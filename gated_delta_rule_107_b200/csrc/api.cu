@@ -863,6 +863,17 @@ static int check_stride(long long stride, long long least, int dtype) {
     return stride % (dtype == DR_BF16 ? 8 : 4) ? DR_ERR_ALIGN : DR_OK;
 }
 
+// A cache's strides: no smaller than a head's channels.
+static int check_cache(long long page, long long token, long long head, int d, int dtype, CacheStrides *st) {
+    const long long all[] = {page, token, head};
+    for (long long x : all) {
+        const int rc = check_stride(x, d, dtype);
+        if (rc != DR_OK) return rc;
+    }
+    *st = {page, token, head};
+    return DR_OK;
+}
+
 // Checks shared by the three forms of the norm with rotation; fills what they share.
 static int check_qkrope(int B, int T, int Hq, int Hk, int d, int rot, int interleaved, int dtype, const void *q,
                         const void *k, const float *wq, const float *wk, const double *inv_freq,
@@ -905,7 +916,9 @@ extern "C" int delta_rule_qkrope_cache(const void *q, const void *k, const void 
                                        const long long *slots, void *q_out, void *k_cache, void *v_cache, int N,
                                        int Hq, int Hk, int d, int rot, int interleaved, long long q_stride,
                                        long long k_stride, long long v_stride, int n_pages, int page,
-                                       long long k_page_stride, long long v_page_stride, int dtype, void *stream) {
+                                       long long k_page_stride, long long k_token_stride, long long k_head_stride,
+                                       long long v_page_stride, long long v_token_stride, long long v_head_stride,
+                                       int dtype, void *stream) {
     QkRope p = {};
     int rc = check_qkrope(1, N, Hq, Hk, d, rot, interleaved, dtype, q, k, wq, wk, inv_freq, positions, q_stride,
                           k_stride, &p);
@@ -913,15 +926,14 @@ extern "C" int delta_rule_qkrope_cache(const void *q, const void *k, const void 
     if (Hk < 1 || n_pages < 0 || page <= 0) return DR_ERR_ARG;
     if (N == 0) return DR_OK;
     if (!positions || !slots || !v || !k_cache || !v_cache || (Hq > 0 && !q_out)) return DR_ERR_ARG;
-    const long long strides[] = {v_stride, k_page_stride, v_page_stride};
-    for (int i = 0; i < 3; ++i) {
-        rc = check_stride(strides[i], (long long)Hk * d * (i == 0 ? 1 : page), dtype);
-        if (rc != DR_OK) return rc;
-    }
+    rc = check_stride(v_stride, (long long)Hk * d, dtype);
+    if (rc == DR_OK) rc = check_cache(k_page_stride, k_token_stride, k_head_stride, d, dtype, &p.kcs);
+    if (rc == DR_OK) rc = check_cache(v_page_stride, v_token_stride, v_head_stride, d, dtype, &p.vcs);
+    if (rc != DR_OK) return rc;
     if (!aligned16(v) || !aligned16(q_out) || !aligned16(k_cache) || !aligned16(v_cache) || (uintptr_t)slots & 7u)
         return DR_ERR_ALIGN;
-    p.v = v; p.vs = v_stride; p.slots = slots; p.qo = q_out; p.kc = k_cache; p.vc = v_cache; p.kps = k_page_stride;
-    p.vps = v_page_stride; p.n_slots = (long long)n_pages * page; p.page = page;
+    p.v = v; p.vs = v_stride; p.slots = slots; p.qo = q_out; p.kc = k_cache; p.vc = v_cache;
+    p.n_slots = (long long)n_pages * page; p.page = page;
     return launch_status(qkrope_run(p, dtype == DR_BF16, (cudaStream_t)stream));
 }
 
@@ -974,16 +986,18 @@ extern "C" size_t delta_rule_attn_decode_workspace_size(int Hq, int Hk, int d, i
 extern "C" int delta_rule_attn_decode(const void *q, const void *k_cache, const void *v_cache, const int *table,
                                       const int *lens, void *out, float *lse, int R, int Hq, int Hk, int d,
                                       int n_pages, int page, int width, long long k_page_stride,
-                                      long long v_page_stride, float scale, int window, int dtype, void *workspace,
-                                      size_t ws_bytes_given, void *stream) {
+                                      long long k_token_stride, long long k_head_stride, long long v_page_stride,
+                                      long long v_token_stride, long long v_head_stride, float scale, int window,
+                                      int dtype, void *workspace, size_t ws_bytes_given, void *stream) {
     int rc = check_attn(Hq, Hk, d, dtype);
     if (rc != DR_OK) return rc;
     if (R < 0 || n_pages < 0 || page <= 0 || width < 0 || window < 0) return DR_ERR_ARG;
     if ((double)R * Hq * ((double)width * page + 64) >= 2199023255552.0) return DR_ERR_UNSUPPORTED;  // the split counts in 32 bits a CTA
     if (R == 0) return DR_OK;
     if (!q || !lens || !out || (width > 0 && !table) || (n_pages > 0 && (!k_cache || !v_cache))) return DR_ERR_ARG;
-    rc = check_stride(k_page_stride, (long long)page * Hk * d, dtype);
-    if (rc == DR_OK) rc = check_stride(v_page_stride, (long long)page * Hk * d, dtype);
+    AttnDecode p = {};
+    rc = check_cache(k_page_stride, k_token_stride, k_head_stride, d, dtype, &p.ks);
+    if (rc == DR_OK) rc = check_cache(v_page_stride, v_token_stride, v_head_stride, d, dtype, &p.vs);
     if (rc != DR_OK) return rc;
     const void *vec[] = {q, k_cache, v_cache, out};
     for (const void *x : vec)
@@ -992,9 +1006,8 @@ extern "C" int delta_rule_attn_decode(const void *q, const void *k_cache, const 
     const bool bf16 = dtype == DR_BF16;
     rc = check_buffer(workspace, ws_bytes_given, attn_decode_ws_bytes(Hq, Hk, d, bf16));
     if (rc != DR_OK) return rc;
-    AttnDecode p = {};
     p.q = q; p.kc = k_cache; p.vc = v_cache; p.table = table; p.lens = lens; p.out = out; p.lse = lse;
-    p.kps = k_page_stride; p.vps = v_page_stride; p.R = R; p.Hq = Hq; p.Hk = Hk; p.d = d; p.page = page;
+    p.R = R; p.Hq = Hq; p.Hk = Hk; p.d = d; p.page = page;
     p.n_pages = n_pages; p.width = width; p.window = window; p.scale = scale; p.ws = workspace;
     return launch_status(attn_decode_run(p, bf16, (cudaStream_t)stream));
 }

@@ -64,7 +64,7 @@ struct Args {
     FastDiv by_page;
     double inv_ctas;     // 1 / CTAs
     bool whole;          // a tile never crosses a page (the page is a multiple of the tile)
-    bool alike;          // both caches' pages are the same distance apart: one offset serves both
+    bool alike;          // both caches have the same strides: one offset serves both
 };
 
 __device__ __forceinline__ uint32_t smem_u32(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
@@ -259,21 +259,20 @@ template <typename E, int D, int TILE_, int STAGES> struct Pipe {
         const bool seen = w.pg >= 0 && w.pg < a.n_pages;
         const uint32_t live = __ballot_sync(0xffffffffu, seen) & ALL;
         const int c = lane % CPR, row0 = lane / CPR, e16 = E16;
-        const size_t inside = ((size_t)w.in * a.Hk + w.h) * D;
-        const size_t ko = seen ? (size_t)w.pg * a.kps + inside : 0;
+        auto offset = [&](const CacheStrides &st) { return (size_t)w.pg * st.page + (size_t)w.in * st.token + (size_t)w.h * st.head; };
+        const size_t ko = seen ? offset(a.ks) : 0;
         if (x.whole && live == ALL) {  // rows of one page: evenly spaced from the first one's
-            const size_t apart = (size_t)a.Hk * D;
-            const E *k = (const E *)a.kc + __shfl_sync(0xffffffffu, ko, 0) + row0 * apart + c * e16;
-            const size_t vo = x.alike ? 0 : (size_t)w.pg * a.vps + inside;
-            const E *v = (const E *)a.vc + __shfl_sync(0xffffffffu, x.alike ? ko : vo, 0) + row0 * apart + c * e16;
+            const size_t kt = a.ks.token, vt = a.vs.token, vo = x.alike ? ko : offset(a.vs);
+            const E *k = (const E *)a.kc + __shfl_sync(0xffffffffu, ko, 0) + row0 * kt + c * e16;
+            const E *v = (const E *)a.vc + __shfl_sync(0xffffffffu, vo, 0) + row0 * vt + c * e16;
 #pragma unroll
             for (int i = 0; i < TILE; i += RPI) {
-                cp16(stage + at(i + row0, c), k + i * apart, true);
-                cp16(stage + HALF + at(i + row0, c), v + i * apart, true);
+                cp16(stage + at(i + row0, c), k + i * kt, true);
+                cp16(stage + HALF + at(i + row0, c), v + i * vt, true);
             }
             return live;
         }
-        const size_t vo = seen && !x.alike ? (size_t)w.pg * a.vps + inside : 0;
+        const size_t vo = seen && !x.alike ? offset(a.vs) : 0;
 #pragma unroll
         for (int i = 0; i < TILE; i += RPI) {
             const int row = i + row0;
@@ -885,7 +884,7 @@ cudaError_t attn_decode_run(const AttnDecode &p, bool bf16, cudaStream_t s) {
     x.G = p.Hq / p.Hk;
     x.scale2 = p.scale * ad::LOG2E;
     x.by_page = FastDiv(p.page);
-    x.alike = p.kps == p.vps;
+    x.alike = p.ks == p.vs;
     const int GB = ad::heads_per_block(x.G, bf16);
     if (!bf16) return p.d == 128 ? ad::simt<128>(x, GB, s) : ad::simt<64>(x, GB, s);
     if (p.d == 128)

@@ -5,13 +5,13 @@
 namespace dr {
 
 // Arguments of one call (device pointers).  q, out [R, Hq, d] and lse [R, Hq] dense; kc, vc pages of
-// `page` tokens [page, Hk, d], kps / vps elements apart; table [R, width]; lens [R].
+// `page` tokens with the strides ks, vs; table [R, width]; lens [R].
 struct AttnDecode {
     const void *q, *kc, *vc;
     const int *table, *lens;
     void *out;
     float *lse;
-    long long kps, vps;
+    CacheStrides ks, vs;
     int R, Hq, Hk, d, page, n_pages, width, window;
     float scale;
     void *ws;

@@ -284,15 +284,15 @@ __global__ void __launch_bounds__(THREADS, 3) k_qkrope(const QkRope p, int hpg) 
         const size_t n = token(n0);
         f2 cs[N2], sn[N2];
         sh.angles(p.pos ? p.pos[n] : (int)((unsigned)n % (unsigned)p.T), j, cs, sn);
-        // heads [from, to) of one tensor, to dst, dense in the head
-        auto run = [&](E *dst, int which, int from, int to) {
+        // heads [from, to) of one tensor, to dst, `apart` from head to head
+        auto run = [&](E *dst, long long apart, int which, int from, int to) {
             if (from >= to) return;
             f2 wA[N2], wB[N2];
             sh.weights(which, j, wA, wB);
             const bool store = act && dst;
-            dst += from * D;
+            dst += from * apart;
 #pragma unroll 1
-            for (int h = from; h < to; ++h, dst += D) {
+            for (int h = from; h < to; ++h, dst += apart) {
                 f2 A[N2], B[N2], ss = 0;
                 ring.wait();
                 open<INTER>(lds16(ring.got), lds16(ring.got + ring.VECTOR), A, B, (E *)nullptr);
@@ -321,17 +321,17 @@ __global__ void __launch_bounds__(THREADS, 3) k_qkrope(const QkRope p, int hpg) 
                 }
             }
         };
-        run((E *)p.qo + n * ((size_t)p.Hq * D), 0, min(h0, p.Hq), min(h1, p.Hq));
+        run((E *)p.qo + n * ((size_t)p.Hq * D), D, 0, min(h0, p.Hq), min(h1, p.Hq));
         E *kdst = CACHE ? nullptr : (E *)p.ko + n * ((size_t)p.Hk * D), *vdst = nullptr;
         if (CACHE) {
             const long long slot = p.slots[n];
             if (slot >= 0 && slot < p.n_slots) {
                 const long long pg = slot / p.page, in = slot - pg * p.page;
-                kdst = (E *)p.kc + pg * p.kps + in * ((long long)p.Hk * D);
-                vdst = (E *)p.vc + pg * p.vps + in * ((long long)p.Hk * D);
+                kdst = (E *)p.kc + pg * p.kcs.page + in * p.kcs.token;
+                vdst = (E *)p.vc + pg * p.vcs.page + in * p.vcs.token;
             }
         }
-        run(kdst, 1, max(h0 - p.Hq, 0), min(h1 - p.Hq, p.Hk));
+        run(kdst, CACHE ? p.kcs.head : D, 1, max(h0 - p.Hq, 0), min(h1 - p.Hq, p.Hk));
         if (CACHE) {
             for (int h = max(h0 - p.Hq - p.Hk, 0); h < h1 - p.Hq - p.Hk; ++h) {
                 ring.wait();
@@ -339,8 +339,8 @@ __global__ void __launch_bounds__(THREADS, 3) k_qkrope(const QkRope p, int hpg) 
                 push();
                 ring.popped();
                 if (act && vdst) {
-                    *reinterpret_cast<uint4 *>(vdst + h * D + l.ia * VEC) = a;
-                    *reinterpret_cast<uint4 *>(vdst + h * D + l.ib * VEC) = b;
+                    *reinterpret_cast<uint4 *>(vdst + h * p.vcs.head + l.ia * VEC) = a;
+                    *reinterpret_cast<uint4 *>(vdst + h * p.vcs.head + l.ib * VEC) = b;
                 }
             }
         }

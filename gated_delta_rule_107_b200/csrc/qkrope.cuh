@@ -8,8 +8,8 @@ namespace dr {
 //   forward   q, k -> qo, ko (dense [N][H][d])
 //   cache     q, k, v -> qo (dense) and the token's slot of kc, vc
 //   backward  q, k, gq, gk (gradients of qo, ko, dense) -> dq, dk (rows dqs, dks apart), dwq, dwk
-// Strides are in elements: from a token to the next (q, k, v, dq, dk; a token's heads are dense),
-// from a page to the next (kc, vc).
+// Strides are in elements: from a token to the next (q, k, v, dq, dk; a token's heads are dense); of
+// kc, vc see CacheStrides.
 struct QkRope {
     const void *q, *k, *v;
     long long qs, ks, vs;
@@ -23,7 +23,8 @@ struct QkRope {
     // cache
     const long long *slots;
     void *kc, *vc;
-    long long kps, vps, n_slots;
+    CacheStrides kcs, vcs;
+    long long n_slots;
     int page;
     // backward
     const void *gq, *gk;

@@ -19,6 +19,14 @@ struct FastDiv {
     __device__ __forceinline__ int div(int n) const { return (int)(((uint64_t)(uint32_t)n * m) >> (31 + s)); }
 };
 
+// Elements of a paged cache from a page, a token, a head to the next (a head's channels are dense).
+struct CacheStrides {
+    long long page, token, head;
+    __host__ __device__ bool operator==(const CacheStrides &o) const {
+        return page == o.page && token == o.token && head == o.head;
+    }
+};
+
 namespace f32x2 {
 // Two fp32 numbers in a 64-bit register pair: Blackwell's packed arithmetic takes one issue slot
 // for both.

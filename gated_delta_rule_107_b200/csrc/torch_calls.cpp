@@ -104,14 +104,17 @@ long long token_stride(const at::Tensor &t, const char *what) {
     return tok;
 }
 
-// Elements from a page to the next of a cache [pages, page, Hk, d], dense inside a page.
-long long page_stride(const at::Tensor &t, const char *what) {
+// Elements from a page, a token and a head to the next of a cache [pages, page, Hk, d] with dense
+// channels (of a dimension of one entry: as if dense).
+struct Strides {
+    long long page, token, head;
+};
+Strides cache_strides(const at::Tensor &t, const char *what) {
     TORCH_CHECK_VALUE(t.dim() == 4, what, ": expected [pages, page, Hk, d], got shape ", t.sizes());
     const auto shape = t.sizes(), st = t.strides();
     const int64_t page = shape[1], H = shape[2], d = shape[3];
-    TORCH_CHECK_VALUE((st[3] == 1 || d == 1) && (H == 1 || st[2] == d) && (page == 1 || st[1] == H * d), what,
-                      " must be dense inside a page, got strides ", st);
-    return shape[0] > 1 ? st[0] : page * H * d;
+    TORCH_CHECK_VALUE(st[3] == 1 || d == 1, what, ": a head's channels must be dense, got strides ", st);
+    return {shape[0] > 1 ? st[0] : page * H * d, page > 1 ? st[1] : H * d, H > 1 ? st[2] : d};
 }
 
 // The call's device and its current stream.
@@ -296,7 +299,8 @@ PyObject *qkrope_cache(PyObject *, Args a, Py_ssize_t n) {
     same_shape(v, "v", x.k.sizes());
     check(kc, "k_cache", type, x.dev);
     check(vc, "v_cache", type, x.dev);
-    const long long vs = token_stride(v, "v"), kps = page_stride(kc, "k_cache"), vps = page_stride(vc, "v_cache");
+    const long long vs = token_stride(v, "v");
+    const Strides ks = cache_strides(kc, "k_cache"), vst = cache_strides(vc, "v_cache");
     TORCH_CHECK_VALUE(kc.sizes() == vc.sizes() && kc.size(2) == x.Hk && kc.size(3) == x.d, "the caches must be [pages, page, ",
                       x.Hk, ", ", x.d, "], got ", kc.sizes(), " and ", vc.sizes());
     const int64_t tokens = (int64_t)x.B * x.T;
@@ -307,8 +311,8 @@ PyObject *qkrope_cache(PyObject *, Args a, Py_ssize_t n) {
     TORCH_CHECK_VALUE(qo.is_contiguous(), "q_out must be contiguous");
     const int rc = c_qkrope_cache(x.q.data_ptr(), x.k.data_ptr(), v.data_ptr(), x.wq, x.wk, x.f, x.pos, (long long *)slots,
                                   qo.data_ptr(), kc.data_ptr(), vc.data_ptr(), extent(tokens, "q"), x.Hq, x.Hk, x.d, x.rot, inter,
-                                  x.qs, x.ks, vs, extent(kc.size(0), "k_cache"), extent(kc.size(1), "k_cache"), kps, vps, x.dtype,
-                                  on.stream);
+                                  x.qs, x.ks, vs, extent(kc.size(0), "k_cache"), extent(kc.size(1), "k_cache"), ks.page, ks.token, ks.head,
+                                  vst.page, vst.token, vst.head, x.dtype, on.stream);
     return rc == DR_OK ? give(qo) : code(rc);
     END_HANDLE_TH_ERRORS
 }
@@ -326,7 +330,7 @@ PyObject *attn_decode(PyObject *, Args a, Py_ssize_t n) {
     const int R = extent(q.size(0), "q"), Hq = extent(q.size(1), "q"), d = extent(q.size(2), "q");
     check(kc, "k_cache", q.scalar_type(), dev);
     check(vc, "v_cache", q.scalar_type(), dev);
-    const long long kps = page_stride(kc, "k_cache"), vps = page_stride(vc, "v_cache");
+    const Strides ks = cache_strides(kc, "k_cache"), vs = cache_strides(vc, "v_cache");
     TORCH_CHECK_VALUE(kc.sizes() == vc.sizes() && kc.size(3) == d, "the caches must be [pages, page, Hk, ", d, "], got ", kc.sizes(),
                       " and ", vc.sizes());
     const int Hk = extent(kc.size(2), "k_cache");
@@ -362,7 +366,8 @@ PyObject *attn_decode(PyObject *, Args a, Py_ssize_t n) {
     if (!ws.defined() || (size_t)ws.numel() < need) ws = empty({(int64_t)need}, at::kByte, dev);
     const int rc = c_attn(qp, kc.data_ptr(), vc.data_ptr(), (int *)tp, (int *)lp, out.data_ptr(),
                           want ? (float *)lse.data_ptr() : nullptr, R, Hq, Hk, d, extent(kc.size(0), "k_cache"),
-                          extent(kc.size(1), "k_cache"), extent(table.size(1), "table"), kps, vps, (float)scale, window, dtype,
+                          extent(kc.size(1), "k_cache"), extent(table.size(1), "table"), ks.page, ks.token, ks.head, vs.page,
+                          vs.token, vs.head, (float)scale, window, dtype,
                           ws.data_ptr(), need, on.stream);
     return rc == DR_OK ? give(out, lse) : code(rc);
     END_HANDLE_TH_ERRORS
@@ -375,10 +380,11 @@ PyObject *stride_of_tokens(PyObject *, Args a, Py_ssize_t n) {
     return PyLong_FromLongLong(token_stride(tensor(a[0], "tensor"), "tensor"));
     END_HANDLE_TH_ERRORS
 }
-PyObject *stride_of_pages(PyObject *, Args a, Py_ssize_t n) {
+PyObject *strides_of_cache(PyObject *, Args a, Py_ssize_t n) {
     HANDLE_TH_ERRORS
     count(n, 1);
-    return PyLong_FromLongLong(page_stride(tensor(a[0], "tensor"), "tensor"));
+    const Strides st = cache_strides(tensor(a[0], "tensor"), "tensor");
+    return Py_BuildValue("LLL", st.page, st.token, st.head);
     END_HANDLE_TH_ERRORS
 }
 
@@ -401,7 +407,7 @@ PyObject *bind(PyObject *, Args a, Py_ssize_t n) {
 
 #define FAST(f) {#f, (PyCFunction)(void (*)(void))f, METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {FAST(bind),        FAST(pages),       FAST(qkrope),           FAST(qkrope_bwd),     FAST(qkrope_cache),
-                         FAST(attn_decode), FAST(stride_of_tokens), FAST(stride_of_pages), {nullptr, nullptr, 0, nullptr}};
+                         FAST(attn_decode), FAST(stride_of_tokens), FAST(strides_of_cache), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_torch_calls", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

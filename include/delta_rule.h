@@ -381,8 +381,10 @@ int delta_rule_clvr_bwd(const void *u, const void *W, const void *dh_out, void *
  *
  * Cache: keys and values in n_pages pages of `page` tokens each,
  *     k_cache, v_cache  [n_pages][page][Hk][d],
- * dense inside a page, consecutive pages k_page_stride / v_page_stride elements
- * apart (>= page * Hk * d, a multiple of 16 bytes: both may lie in one buffer).
+ * a head's d channels dense, and the elements from a page, a token and a head to
+ * the next as given (k_page_stride, k_token_stride, k_head_stride, v_...; each
+ * >= d and a multiple of 16 bytes): tokens or heads may come first in a page, keys
+ * and values may share a buffer.  Rows must not overlap.
  * A request's tokens are found through its row of the block table
  * table [R][width] (int32): token t is row t % page of page table[r][t / page].
  * The slot of a token is its page's number * page + its row (int64).
@@ -405,7 +407,8 @@ int delta_rule_clvr_bwd(const void *u, const void *W, const void *dh_out, void *
  * short the table entry and the slots are -1; likewise the slots of tokens
  * behind the table's width (no page is taken for those).  N <= 2^30.  n_left
  * must not be n_free itself; the stack's entries are not changed, so the next
- * step passes n_left as its n_free.
+ * step passes n_left as its n_free.  A request that ends gives its pages back when
+ * the caller writes their numbers behind the top and raises the count.
  */
 int delta_rule_pages(const int *cached, const int *fresh, const int *free_pages, const int *n_free, int *table,
                      int *lens, int *cu_new, int *positions, long long *slots, int *n_left, int R, int F, int width,
@@ -452,7 +455,9 @@ int delta_rule_qkrope_cache(const void *q, const void *k, const void *v, const f
                             const double *inv_freq, const int *positions, const long long *slots, void *q_out,
                             void *k_cache, void *v_cache, int N, int Hq, int Hk, int d, int rot, int interleaved,
                             long long q_stride, long long k_stride, long long v_stride, int n_pages, int page,
-                            long long k_page_stride, long long v_page_stride, int dtype, void *stream);
+                            long long k_page_stride, long long k_token_stride, long long k_head_stride,
+                            long long v_page_stride, long long v_token_stride, long long v_head_stride, int dtype,
+                            void *stream);
 
 /*
  * Attention of one new token per request over the paged cache.  q [R,Hq,d] is
@@ -472,8 +477,10 @@ int delta_rule_qkrope_cache(const void *q, const void *k, const void *v, const f
 size_t delta_rule_attn_decode_workspace_size(int Hq, int Hk, int d, int dtype);
 int delta_rule_attn_decode(const void *q, const void *k_cache, const void *v_cache, const int *table,
                            const int *lens, void *out, float *lse, int R, int Hq, int Hk, int d, int n_pages,
-                           int page, int width, long long k_page_stride, long long v_page_stride, float scale,
-                           int window, int dtype, void *workspace, size_t ws_bytes, void *stream);
+                           int page, int width, long long k_page_stride, long long k_token_stride,
+                           long long k_head_stride, long long v_page_stride, long long v_token_stride,
+                           long long v_head_stride, float scale, int window, int dtype, void *workspace,
+                           size_t ws_bytes, void *stream);
 
 /*
  * Self-test of failure detection.  Launches one kernel on `stream` whose bounded

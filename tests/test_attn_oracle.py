@@ -127,8 +127,8 @@ def test_qkrope_refusals(lib):
                Hq=4, Hk=2, d=128, rot=128, interleaved=0, qs=1024, ks=1024, dqs=1024, dks=1024, dtype=b.DR_BF16, ws=A,
                nws=1 << 30)
     cache = dict(q=A, k=A, v=A, wq=A, wk=A, inv_freq=A, positions=A, slots=A, q_out=A, kc=A, vc=A, N=5, Hq=4, Hk=2,
-                 d=128, rot=128, interleaved=0, qs=1024, ks=1024, vs=1024, n_pages=3, page=16, kps=4096, vps=4096,
-                 dtype=b.DR_BF16)
+                 d=128, rot=128, interleaved=0, qs=1024, ks=1024, vs=1024, n_pages=3, page=16, kps=4096, kts=256, khs=128,
+                 vps=4096, vts=256, vhs=128, dtype=b.DR_BF16)
     calls = ((fwd, b.qkrope_raw), (bwd, b.qkrope_bwd_raw), (cache, b.qkrope_cache_raw))
     for ok, fn in calls:
         def call(**kw):
@@ -144,8 +144,8 @@ def test_qkrope_refusals(lib):
         assert call(rot=256) == b.DR_ERR_ARG and call(rot=-16) == b.DR_ERR_ARG and call(interleaved=2) == b.DR_ERR_ARG
         assert call(dtype=7) == b.DR_ERR_ARG and call(Hq=-1) == b.DR_ERR_ARG
         assert call(Hq=1020, Hk=8) == b.DR_ERR_UNSUPPORTED
-        for name in set(ok) & {"qs", "ks", "vs", "dqs", "dks", "kps", "vps"}:
-            assert call(**{name: 64}) == b.DR_ERR_ARG, name       # shorter than a token's heads
+        for name in set(ok) & {"qs", "ks", "vs", "dqs", "dks", "kps", "kts", "khs", "vps", "vts", "vhs"}:
+            assert call(**{name: 64}) == b.DR_ERR_ARG, name       # shorter than a token's heads, or a head
             assert call(**{name: 8196}) == b.DR_ERR_ALIGN, name   # rows off 16 bytes
     def wcall(**kw):
         return b.qkrope_bwd_raw(*{**bwd, **kw}.values(), None)
@@ -163,7 +163,7 @@ def test_qkrope_refusals(lib):
 def test_attn_decode_refusals(lib):
     from gated_delta_rule_107_b200 import binding as b
     ok = dict(q=A, kc=A, vc=A, table=A, lens=A, out=A, lse=A, R=2, Hq=8, Hk=2, d=128, n_pages=4, page=16, width=2,
-              kps=4096, vps=4096, scale=1.0, window=0, dtype=b.DR_BF16, ws=A, nws=1 << 30)
+              kps=4096, kts=256, khs=128, vps=4096, vts=256, vhs=128, scale=1.0, window=0, dtype=b.DR_BF16, ws=A, nws=1 << 30)
 
     def call(**kw):
         return b.attn_decode_raw(*{**ok, **kw}.values(), None)
@@ -175,9 +175,11 @@ def test_attn_decode_refusals(lib):
     for name in ("table", "lens", "lse"):
         assert call(**{name: A + 2}) == b.DR_ERR_ALIGN, name
     for bad in (dict(R=-1), dict(Hq=0), dict(Hk=0), dict(Hq=7), dict(n_pages=-1), dict(page=0), dict(width=-1),
-                dict(window=-1), dict(dtype=3), dict(kps=2048), dict(vps=2048)):
+                dict(window=-1), dict(dtype=3), dict(kps=64), dict(vps=64), dict(kts=120), dict(vts=0), dict(khs=-128), dict(vhs=64)):
         assert call(**bad) == b.DR_ERR_ARG, bad
-    assert call(d=96) == b.DR_ERR_UNSUPPORTED and call(kps=4100) == b.DR_ERR_ALIGN
+    assert call(d=96) == b.DR_ERR_UNSUPPORTED
+    for name in ("kps", "kts", "khs", "vps", "vts", "vhs"):
+        assert call(**{name: 4100}) == b.DR_ERR_ALIGN, name
     assert call(R=1 << 20, width=1 << 18, page=16) == b.DR_ERR_UNSUPPORTED
     need = lib.delta_rule_attn_decode_workspace_size(8, 2, 128, b.DR_BF16)
     assert call(ws=None) == b.DR_ERR_WORKSPACE and call(nws=need - 1) == b.DR_ERR_WORKSPACE
@@ -198,7 +200,7 @@ def test_python_level_refusals():
         b.delta_rule_attn_decode(x, x, x, x, x)
     with pytest.raises(ValueError):
         b.delta_rule_pages(x, x, x, x, x, 16, 4)
-    tok, pg = b._calls().stride_of_tokens, b._calls().stride_of_pages
+    tok, cs = b._calls().stride_of_tokens, b._calls().strides_of_cache
     assert tok(torch.zeros(5, 6 * 64).unflatten(-1, (6, 64))[:, 2:4]) == 384
     assert tok(torch.zeros(2, 5, 6, 64)[:, :, 1:3]) == 384
     assert tok(torch.zeros(2, 5, 6, 64)[:, :1]) == 5 * 384
@@ -207,11 +209,13 @@ def test_python_level_refusals():
                 torch.zeros(6, 64), torch.zeros(5, 6, 128)[..., :64]):
         with pytest.raises(ValueError):
             tok(bad)
-    assert pg(torch.zeros(4, 2, 16, 2, 64)[:, 1]) == 2 * 16 * 2 * 64
-    assert pg(torch.zeros(1, 2, 16, 2, 64)[:, 1]) == 16 * 2 * 64
-    for bad in (torch.zeros(4, 16, 4, 64)[:, :, 1:3], torch.zeros(4, 2, 16, 64).transpose(1, 2), torch.zeros(4, 16, 64)):
+    assert cs(torch.zeros(4, 2, 16, 2, 64)[:, 1]) == (2 * 16 * 2 * 64, 128, 64)
+    assert cs(torch.zeros(1, 2, 16, 2, 64)[:, 1]) == (16 * 2 * 64, 128, 64)
+    assert cs(torch.zeros(4, 2, 16, 64).transpose(1, 2)) == (2 * 16 * 64, 64, 16 * 64)  # heads first
+    assert cs(torch.zeros(4, 16, 4, 64)[:, :, 1:3]) == (16 * 256, 256, 64)
+    for bad in (torch.zeros(4, 16, 64), torch.zeros(4, 16, 2, 128)[..., ::2], torch.zeros(4, 16, 64, 2).transpose(2, 3)):
         with pytest.raises(ValueError):
-            pg(bad)
+            cs(bad)
     with pytest.raises(TypeError):
         tok(3)
     with pytest.raises(TypeError):

@@ -299,19 +299,21 @@ def test_qkrope_captured_backward_beside_eager_calls():
 # ------------------------------------------------------------------------------------ into the cache
 @pytest.mark.parametrize("dtype", ("f32", "bf16"))
 @pytest.mark.parametrize("N,Hq,Hk,d,page,joint", ((1, 4, 1, 128, 16, False), (7, 2, 2, 64, 7, True), (300, 16, 2, 128, 64, True),
-                                                  (1000, 3, 3, 64, 1, False)))
+                                                  (1000, 3, 3, 64, 1, False), (130, 2, 4, 64, 16, "heads first")))
 def test_qkrope_cache(dtype, N, Hq, Hk, d, page, joint):
     q, k, v, (wq, wk), f, pos = _qk_case(dtype, 1, N, Hq, Hk, d, d // 2, seed=N)
     q, k, v, pos = q[0], k[0], v[0], pos[0].contiguous()
     P = -(-N // page) + 3
     g = _rng(N)
     both = _randn(g, P, 2, page, Hk, d, dtype=dtype)
-    kc, vc = (both[:, 0], both[:, 1]) if joint else (both[:, 0].contiguous(), both[:, 1].contiguous())
+    kc, vc = (both[:, 0], both[:, 1]) if joint is True else (both[:, 0].contiguous(), both[:, 1].contiguous())
+    if joint == "heads first":
+        kc, vc = (t.transpose(1, 2).contiguous().transpose(1, 2) for t in (kc, vc))
     slots = torch.randperm(P * page, generator=g)[:N]
     skip = torch.rand(N, generator=g) < 0.2
     slots[skip] = torch.tensor([-1, -7, P * page, 2 ** 40])[torch.randint(0, 4, (int(skip.sum()),), generator=g)]
     slots = slots.cuda()
-    k0, v0 = kc.clone(), vc.clone()
+    k0, v0 = kc.clone(memory_format=torch.contiguous_format), vc.clone(memory_format=torch.contiguous_format)
     qo = binding.delta_rule_qkrope_cache(q, k, v, wq, wk, f, pos, slots, kc, vc)
     torch.cuda.synchronize()
     want_q, want_k = binding.delta_rule_qkrope(q, k, wq, wk, f, pos)
@@ -428,6 +430,15 @@ def test_attn_decode_caches_of_different_strides(dtype, page):
     torch.cuda.synchronize()
     _check_attn(*want, q, kc, vc, table, lens, dtype)
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    # heads before tokens; heads before pages, in one of the two; a slice of more heads
+    hnd = lambda t: t.permute(0, 2, 1, 3).contiguous().permute(0, 2, 1, 3)  # noqa: E731
+    first = vc.permute(2, 0, 1, 3).contiguous().permute(1, 2, 0, 3)
+    wide = torch.full((P, page, 5, 128), float("nan"), dtype=DT[dtype], device="cuda")
+    wide[:, :, 2:4] = kc
+    for k2, v2 in ((hnd(kc), hnd(vc)), (kc, first), (wide[:, :, 2:4], hnd(vc))):
+        got = binding.delta_rule_attn_decode(q, k2, v2, table, _i32(lens), want_lse=True)
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
 def test_attn_decode_without_pages_or_table():
@@ -676,7 +687,8 @@ def test_python_level_refusals_on_cuda_tensors():
     binding.delta_rule_attn_decode(**attn)
     for bad in (dict(q=x.bfloat16()), dict(table=table.long()), dict(table=table[:3]), dict(lens=lens[:3]), dict(lens=lens.long()),
                 dict(q=x[:, :, ::2]), dict(k_cache=kc.transpose(1, 2)), dict(v_cache=kc[:3]), dict(out=x.bfloat16()),
-                dict(workspace=x), dict(q=x[0]), dict(table=_i32([[0] * 4] * 4)[:, ::2])):
+                dict(workspace=x), dict(q=x[0]), dict(table=_i32([[0] * 4] * 4)[:, ::2]),
+                dict(k_cache=torch.zeros(5, 16, 64, 2, device="cuda").transpose(2, 3))):
         with pytest.raises(ValueError):
             binding.delta_rule_attn_decode(**{**attn, **bad})
     for bad, want in ((dict(q=x[:, :5].contiguous()), binding.DR_ERR_ARG), (dict(window=-1), binding.DR_ERR_ARG)):
