@@ -17,12 +17,12 @@
 //
 // What bounds it is moving each element twice (forward) or three times (backward).  At 8 x 4096
 // tokens of 10 heads of 128 channels in bf16: forward 30.3 us for 168 MB (5.5 TB/s, 86 % of a plain
-// copy's rate), backward 46.4 us for 252 MB (84 %); 8192 tokens of 16 + 2 + 2 heads into the cache
+// copy's rate), backward 45.5 us for 252 MB (86 %); 8192 tokens of 16 + 2 + 2 heads into the cache
 // 14.2 us for 84 MB (91 %).  To get there the loads run ahead through shared memory (with loads into
 // registers the forward took 50.8 us, its warps waiting), the arithmetic is packed (without, 70 % of
 // all issue slots were taken), and neighbouring lanes always hold neighbouring vectors (with the
 // channels behind rot two vectors a lane side by side, 32768 tokens with half of the channels
-// rotated took 118 us backward instead of 87).
+// rotated took 118 us backward instead of 86).
 #include <type_traits>
 
 #include "qkrope.cuh"
@@ -505,7 +505,13 @@ template <int D> __global__ void __launch_bounds__(1024) k_qkrope_dw(const float
     after_previous();
     const int cx = threadIdx.x & 31, ry = threadIdx.x >> 5, col = blockIdx.x * 32 + cx;
     float s = 0.f;
-    for (int r = ry; r < n; r += 32) s += part[(size_t)r * 2 * D + col];
+    for (int r = ry; r < n; r += 32 * 10) {  // all of a thread's partials at once: at most BWD_CTAS / 32
+        float x[10];
+#pragma unroll
+        for (int k = 0; k < 10; ++k) x[k] = r + 32 * k < n ? part[(size_t)(r + 32 * k) * 2 * D + col] : 0.f;
+#pragma unroll
+        for (int k = 0; k < 10; ++k) s += x[k];
+    }
     red[ry][cx] = s;
     __syncthreads();
     s = warp_sum(red[cx][ry]);  // warp ry: column ry of the CTA's 32
@@ -540,7 +546,7 @@ template <typename E, int D, bool INTER> static cudaError_t fwd(const QkRope &p,
 
 template <typename E, int D, bool INTER> static cudaError_t bwd(const QkRope &p, cudaStream_t s) {
     // one wave of CTAs with equal runs: each CTA's sums of the weights' gradients cost it a reduction
-    // (8 x 4096 tokens: 46.4 us; a warp for every tokens' heads, 1024 CTAs, 53.5)
+    // (8 x 4096 tokens: 45.5 us; a warp for every tokens' heads, 1024 CTAs, 53.5)
     constexpr int TPW = Lay<E, D, INTER>::TPW, WARPS = BWD_CTAS * (THREADS / 32);
     const long long items = (long long)((p.N + TPW - 1) / TPW) * (p.Hq + p.Hk), per = (items + WARPS - 1) / WARPS;
     const int ctas = (int)((items + per * (THREADS / 32) - 1) / (per * (THREADS / 32)));
