@@ -1,6 +1,7 @@
 """The fp64 reference of the softmax-attention operators (oracle/attn.py) against hand-worked
 examples, identities and differences, and the entry points' refusals, without a GPU."""
 import ctypes
+import types
 
 import numpy as np
 import pytest
@@ -89,6 +90,47 @@ def test_attention_identities():
     ob, _ = oa.attn_decode(q, kc, vc, np.array([[9, 1, 5], [0, 2, -1], [3, 3, 3]]), [6, 5, 0])
     s = k[3:6, 0] @ q[0, 0] / 2.0                              # page 9 is no page: tokens 3 .. 5 remain
     assert np.allclose(ob[0, 0], np.exp(s) @ v[3:6, 0] / np.exp(s).sum())
+
+
+# ------------------------------------------------------------------------------------ planted mistakes
+PINS = ([test_pages_hand_example, test_pages_short_stack_and_narrow_table, test_qkrope_quarter_turn, test_attention_identities]
+        + [lambda r=r, i=i: test_qkrope_identities(r, i) for r in (0, 4, 8) for i in (False, True)]
+        + [lambda i=i: test_qkrope_gradient_against_differences(i) for i in (False, True)])
+MUTANTS = [
+    ("pages_from_the_bottom", "table[r, j] = free_pages[left] if left >= 0 else -1", "table[r, j] = free_pages[top - 1 - left] if left >= 0 else -1"),
+    ("partial_page_dropped", "for j in range(min(ceil_div(a, page), width)", "for j in range(min(a // page, width)"),
+    ("slot_without_row", "table[r, p // page] * page + p % page if ok", "table[r, p // page] * page if ok"),
+    ("position_from_zero", "            positions.append(p)", "            positions.append(p - a)"),
+    ("norm_without_root", "    y = x / np.sqrt((x * x).mean(-1, keepdims=True) + EPS)", "    y = x / ((x * x).mean(-1, keepdims=True) + EPS)"),
+    ("sum_for_mean", "    y = x / np.sqrt((x * x).mean(-1, keepdims=True) + EPS)", "    y = x / np.sqrt((x * x).sum(-1, keepdims=True) + EPS)"),
+    ("pairs_exchanged", "return (2 * i, 2 * i + 1) if interleaved else (i, i + rot // 2)", "return (i, i + rot // 2) if interleaved else (2 * i, 2 * i + 1)"),
+    ("turned_backwards", "a * c - b * s, b * c + a * s", "a * c + b * s, b * c - a * s"),
+    ("gradient_not_turned_back", "np.asarray(dy, np.float64), positions, inv_freq, interleaved, -1.0)", "np.asarray(dy, np.float64), positions, inv_freq, interleaved, 1.0)"),
+    ("gradient_without_projection", "(gn - n * (gn * n).mean(-1, keepdims=True)) / rms", "gn / rms"),
+    ("weight_missing_in_gradient", "    gn = g if w is None else g * w\n", "    gn = g\n"),
+    ("scale_missing", "s = scale * (k[:, h // G] @ q[r, h])", "s = k[:, h // G] @ q[r, h]"),
+    ("group_of_heads", "s = scale * (k[:, h // G] @ q[r, h])", "s = scale * (k[:, h % Hk] @ q[r, h])"),
+    ("window_ignored", "np.arange(max(0, n - window) if window else 0, n)", "np.arange(0, n)"),
+    ("last_token_missing", "np.arange(max(0, n - window) if window else 0, n)", "np.arange(max(0, n - window) if window else 0, max(n - 1, 0))"),
+    ("bad_page_seen", "ok = (pg >= 0) & (pg < n_pages)", "pg = pg % n_pages; ok = pg >= 0"),
+    ("lse_without_maximum", "lse[r, h] = m + np.log(p.sum())", "lse[r, h] = np.log(p.sum())"),
+]
+
+
+@pytest.mark.parametrize("name,old,new", MUTANTS, ids=[m[0] for m in MUTANTS])
+def test_mutant_is_caught(name, old, new, monkeypatch):
+    src = open(oa.__file__).read()
+    assert src.count(old) == 1, f"mutation site for {name}"
+    mod = types.ModuleType(f"attn_{name}")
+    exec(compile(src.replace(old, new), f"<{name}>", "exec"), mod.__dict__)
+    monkeypatch.setitem(globals(), "oa", mod)
+    caught = 0
+    for pin in PINS:
+        try:
+            pin()
+        except (AssertionError, ValueError, IndexError):
+            caught += 1
+    assert caught > 0, f"no pin catches {name}"
 
 
 # ------------------------------------------------------------------------------------ refusals
