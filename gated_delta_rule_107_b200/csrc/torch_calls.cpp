@@ -189,6 +189,7 @@ PyObject *pages(PyObject *, Args a, Py_ssize_t n) {
     void *cp = dense(cached, "cached", at::kInt, dev, -1), *fp = dense(fresh, "fresh", at::kInt, dev, R),
          *sp = dense(stack, "free_pages", at::kInt, dev, -1), *np = dense(n_free, "n_free", at::kInt, dev, 1),
          *tp = dense(table, "table", at::kInt, dev, -1);
+    if (R > 8192 || N > 1 << 30) return code(DR_ERR_UNSUPPORTED);  // before gigabytes are allocated for the refusal
     On on(dev);
     Together t(12ll * N + 8ll * R + 8, dev);  // the 8-byte elements first
     const at::Tensor slots = t.next(at::kLong, {N}), pos = t.next(at::kInt, {N}), lens = t.next(at::kInt, {R}),

@@ -704,6 +704,13 @@ def test_python_level_refusals_on_cuda_tensors():
             binding.delta_rule_pages(**{**pages, **bad})
     with pytest.raises(binding.DeltaRuleError):
         binding.delta_rule_pages(**{**pages, "page": 0})
+    for bad in (dict(tokens=2 ** 31 - 1), dict(cached=torch.zeros(8193, dtype=torch.int32, device="cuda"),
+                                               fresh=torch.zeros(8193, dtype=torch.int32, device="cuda"),
+                                               table=torch.zeros(8193, 1, dtype=torch.int32, device="cuda"))):
+        before = torch.cuda.max_memory_reserved()
+        with pytest.raises(binding.DeltaRuleError) as e:
+            binding.delta_rule_pages(**{**pages, **bad})
+        assert e.value.code == binding.DR_ERR_UNSUPPORTED and torch.cuda.max_memory_reserved() == before
     torch.cuda.synchronize()
 
 
