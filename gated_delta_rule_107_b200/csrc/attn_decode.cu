@@ -29,10 +29,12 @@
 //     columns: S^T = K Q^T, then o^T = V^T P^T with P^T transposed in registers.  A group of up to
 //     8 heads is one n8 column block, of 16 two (larger groups are taken 16 heads at a time, and
 //     their rows read again for each block), so no row is spent on padding to 16 heads, and tcgen05's
-//     smallest tile (64 or 128 rows through tensor memory) would be mostly padding.  P is split
-//     into two bf16 numbers (high and rest, 2^-17 of p) and multiplied twice: rounding P once
-//     would put as large an error in the output as its own rounding, and the second product is
-//     hidden behind the loads.  Groups of 16 reach 83 to 90 % of the copy's rate, of 32 45 %.
+//     smallest tile (64 or 128 rows through tensor memory) would be mostly padding.  P enters with
+//     all of its 24 bits, as three bf16 numbers of 8 bits each that are multiplied one after another:
+//     with two of them (2^-17 of p) outputs that are small against the values were off by more than
+//     fp32 sums are, and the third product is hidden behind the loads (three requests of 200001 tokens
+//     186.5 -> 187.6 us, 64 of up to 16384 91.4 -> 91.0, one of 2000 7.5 -> 7.8).  Groups of 16 reach
+//     83 to 90 % of the copy's rate, of 32 45 %.
 //   fp32.  CUDA cores, 1, 2, 4 or up to 8 heads at a time, packed arithmetic: a lane holds 4 channels
 //     of the heads' queries and outputs.  Groups of up to 4 are bound by the loads (87 to 94 % of the
 //     copy's rate), of 8 by two warps a scheduler working through their tiles (68 to 70 %).
@@ -97,9 +99,9 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-__device__ __forceinline__ uint32_t pack(float lo, float hi) {
-    const __nv_bfloat162 x = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t *>(&x);
+// the upper halves of two fp32 numbers: each one's first 8 bits as a bf16 number
+__device__ __forceinline__ uint32_t upper(float lo, float hi) {
+    return __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x7632);
 }
 
 // log of the sum l (base 2 maximum m); nothing seen: -inf; a NaN stays
@@ -298,6 +300,7 @@ __device__ __forceinline__ int slot_of(int head, int ch) { return ch ^ ((head >>
 template <int D, int NT> struct Mma {  // bf16: blocks of 8 NT heads
     typedef __nv_bfloat16 E;
     static constexpr int GB = 8 * NT, STAGES = 3, CTAS = MAX_CTAS, SUB = 128 / D;  // 16 SUB tokens a tile
+    static constexpr int NPART = 3;  // bf16 numbers that make up a weight: 8 bits each of its 24
     typedef Pipe<E, D, 16 * SUB, STAGES> P;
     uint32_t q[D / 16][NT][2], qn[D / 16][NT][2];
     float o[D / 16][NT][4], m[NT][2], l[NT][2];
@@ -397,24 +400,22 @@ template <int D, int NT> struct Mma {  // bf16: blocks of 8 NT heads
         const int row = (lane & 7) + ((lane >> 4) << 3), c0 = lane >> 3 & 1;
 #pragma unroll
         for (int u = 0; u < SUB; ++u) {
-            uint32_t ph[NT][2], pl[NT][2];
+            uint32_t part[NPART][NT][2];
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
-                float p[4], rest[4];
+                float p[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     // -inf minus -inf (nothing seen yet) must not be NaN
                     p[i] = s[u][j][i] == -CUDART_INF_F ? 0.f : ex2(s[u][j][i] - m[j][i & 1]);
                     l[j][i & 1] += p[i];
                 }
-                ph[j][0] = pack(p[0], p[1]);
-                ph[j][1] = pack(p[2], p[3]);
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    rest[2 * i] = p[2 * i] - __uint_as_float(ph[j][i] << 16);
-                    rest[2 * i + 1] = p[2 * i + 1] - __uint_as_float(ph[j][i] & 0xFFFF0000u);
-                    pl[j][i] = trans8(pack(rest[2 * i], rest[2 * i + 1]));
-                    ph[j][i] = trans8(ph[j][i]);
+                for (int x = 0; x < NPART; ++x) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) part[x][j][i] = trans8(upper(p[2 * i], p[2 * i + 1]));
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) p[i] -= __uint_as_float(__float_as_uint(p[i]) & 0xFFFF0000u);
                 }
             }
             const uint32_t v = stage + P::HALF;
@@ -423,10 +424,9 @@ template <int D, int NT> struct Mma {  // bf16: blocks of 8 NT heads
                 uint32_t a[4];
                 ldsm4t(a, v + P::at(u * 16 + row, 2 * k + c0));
 #pragma unroll
-                for (int j = 0; j < NT; ++j) {
-                    mma(o[k][j], a, ph[j][0], ph[j][1]);
-                    mma(o[k][j], a, pl[j][0], pl[j][1]);
-                }
+                for (int j = 0; j < NT; ++j)
+#pragma unroll
+                    for (int x = 0; x < NPART; ++x) mma(o[k][j], a, part[x][j][0], part[x][j][1]);
             }
         }
     }

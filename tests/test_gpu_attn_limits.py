@@ -1,0 +1,45 @@
+"""The softmax-attention layers' operators at the limits of their arithmetic, sizes and arguments:
+what a comparison at ordinary inputs does not show.  Each tolerance is derived where it is used."""
+import numpy as np
+import pytest
+import torch
+
+from gated_delta_rule_107_b200 import binding
+from oracle import attn as oa
+from parity_util import np64
+from test_gpu_attn import DT, HALF, _i32
+
+pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------------------------------------------------ attention
+@pytest.mark.parametrize("dtype", ("f32", "bf16"))
+@pytest.mark.parametrize("d,Hq,Hk,tiles", ((64, 3, 1, 1), (128, 3, 1, 1), (128, 12, 1, 40), (64, 32, 2, 40)))
+def test_attn_decode_weights_keep_32_bits(dtype, d, Hq, Hk, tiles):
+    """Values that cancel, so that the output is what the weights' rounding leaves.
+
+    Of every 16 tokens 14 have the score -5/4 and the value 1, two the score 0 and values whose sum is
+    minus what the 14 weights add up to.  e^-1.25 as a sum of two bf16 numbers would be off by 2^-17.2.
+    In 32 bits: the score in base 2 is off by 2.25 x 2^-24 (scale log2 e and the product, rounded), so
+    the weight by 2^-23.3, and by the exponential's 2^-22: together 2^-21.5; 16 addends, each cut or
+    rounded at 2^-24 of the largest, 2^-20; all relative to the sum of the 14.  The tiles' sums cancel
+    each for itself, so their errors add up as their weights do, and the ratio stays."""
+    n = 16 * tiles
+    p = np.exp(-1.25)
+    x1 = torch.tensor(14 * p, dtype=torch.bfloat16)
+    x2 = torch.tensor(14 * p - x1.double().item(), dtype=torch.bfloat16)
+    kc, vc = (torch.zeros(tiles, 16, Hk, d, dtype=DT[dtype], device="cuda") for _ in range(2))
+    q = torch.zeros(1, Hq, d, dtype=DT[dtype], device="cuda")
+    q[..., 0] = 1.0
+    kc[:, :, :, 0] = -1.25
+    vc[:] = 1.0
+    kc[:, 5], kc[:, 11] = 0.0, 0.0
+    vc[:, 5], vc[:, 11] = -x1.item(), -x2.item()
+    table = torch.arange(tiles, dtype=torch.int32, device="cuda")[None]
+    o, lse = binding.delta_rule_attn_decode(q, kc, vc, table, _i32([n]), scale=1.0, want_lse=True)
+    torch.cuda.synchronize()
+    ref, ref_lse = oa.attn_decode(np64(q), np64(kc), np64(vc), table.cpu().numpy(), [n], 1.0)
+    tol = 14 * p / (14 * p + 2) * (2.0 ** -21.5 + 2.0 ** -20) + HALF[dtype] * np.abs(ref)
+    worst = (np.abs(np64(o) - ref) / tol).max()
+    assert worst <= 1, f"{worst} x tol"
+    assert np.abs(np64(lse) - ref_lse).max() <= 2.0 ** -20 + (n / 16 + 8) * 2.0 ** -23
