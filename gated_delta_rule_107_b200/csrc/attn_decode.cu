@@ -30,11 +30,14 @@
 //     8 heads is one n8 column block, of 16 two (larger groups are taken 16 heads at a time, and
 //     their rows read again for each block), so no row is spent on padding to 16 heads, and tcgen05's
 //     smallest tile (64 or 128 rows through tensor memory) would be mostly padding.  P enters with
-//     all of its 24 bits, as three bf16 numbers of 8 bits each that are multiplied one after another:
-//     with two of them (2^-17 of p) outputs that are small against the values were off by more than
-//     fp32 sums are, and the third product is hidden behind the loads (three requests of 200001 tokens
-//     186.5 -> 187.6 us, 64 of up to 16384 91.4 -> 91.0, one of 2000 7.5 -> 7.8).  Groups of 16 reach
-//     83 to 90 % of the copy's rate, of 32 45 %.
+//     all of its 24 bits, as three bf16 numbers of 8 bits each that are multiplied one after another
+//     (with two, 2^-17 of p, outputs that are small against the values were off by more than fp32 sums
+//     are), and a tile's products are summed from zero and then added to o in fp32: the tensor cores
+//     cut what they add to a sum, and cutting the running sum a thousand times lost 2^-16 of it.  The
+//     additional products hide behind the loads, less so in wide groups (three requests of 200001
+//     tokens 186 -> 187 us, 64 of up to 16384 91.0 -> 91.5, one of 2000 7.5 -> 7.9; 32 of 6103 with
+//     groups of 16 29.8 -> 31.5, with 64 channels 21.8 -> 23.4).  Groups of 16 reach 79 to 83 % of the
+//     copy's rate, of 32 43 %.
 //   fp32.  CUDA cores, 1, 2, 4 or up to 8 heads at a time, packed arithmetic: a lane holds 4 channels
 //     of the heads' queries and outputs.  Groups of up to 4 are bound by the loads (87 to 94 % of the
 //     copy's rate), of 8 by two warps a scheduler working through their tiles (68 to 70 %).
@@ -303,7 +306,8 @@ template <int D, int NT> struct Mma {  // bf16: blocks of 8 NT heads
     static constexpr int NPART = 3;  // bf16 numbers that make up a weight: 8 bits each of its 24
     typedef Pipe<E, D, 16 * SUB, STAGES> P;
     uint32_t q[D / 16][NT][2], qn[D / 16][NT][2];
-    float o[D / 16][NT][4], m[NT][2], l[NT][2];
+    f2 o[D / 16][NT][2];  // heads 2 t and 2 t + 1 of channel g, of channel g + 8
+    float m[NT][2], l[NT][2];
 
     __device__ __forceinline__ void fetch(const E *src, int heads) {
         const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -326,7 +330,7 @@ template <int D, int NT> struct Mma {  // bf16: blocks of 8 NT heads
             for (int k = 0; k < D / 16; ++k) {
                 q[k][j][0] = qn[k][j][0];
                 q[k][j][1] = qn[k][j][1];
-                o[k][j][0] = o[k][j][1] = o[k][j][2] = o[k][j][3] = 0.f;
+                o[k][j][0] = o[k][j][1] = 0;
             }
         }
     }
@@ -378,29 +382,23 @@ template <int D, int NT> struct Mma {  // bf16: blocks of 8 NT heads
                 mx[j][0] = fmaxf(mx[j][0], __shfl_xor_sync(0xffffffffu, mx[j][0], d));
                 mx[j][1] = fmaxf(mx[j][1], __shfl_xor_sync(0xffffffffu, mx[j][1], d));
             }
-        bool up = false;
+        f2 f[NT];
 #pragma unroll
-        for (int j = 0; j < NT; ++j) up = up || mx[j][0] > m[j][0] || mx[j][1] > m[j][1];
-        if (__any_sync(0xffffffffu, up)) {
+        for (int j = 0; j < NT; ++j) {
+            float fj[2];
 #pragma unroll
-            for (int j = 0; j < NT; ++j)
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const float mn = fmaxf(m[j][i], mx[j][i]);
-                    const float f = m[j][i] == mn ? 1.f : ex2(m[j][i] - mn);  // equal: both may be -inf
-                    m[j][i] = mn;
-                    l[j][i] *= f;
-#pragma unroll
-                    for (int k = 0; k < D / 16; ++k) {
-                        o[k][j][i] *= f;
-                        o[k][j][i + 2] *= f;
-                    }
-                }
+            for (int i = 0; i < 2; ++i) {
+                const float mn = fmaxf(m[j][i], mx[j][i]);
+                fj[i] = m[j][i] == mn ? 1.f : ex2(m[j][i] - mn);  // equal: both may be -inf
+                m[j][i] = mn;
+                l[j][i] *= fj[i];
+            }
+            f[j] = mk(fj[0], fj[1]);
         }
         const int row = (lane & 7) + ((lane >> 4) << 3), c0 = lane >> 3 & 1;
+        uint32_t part[SUB][NPART][NT][2];
 #pragma unroll
-        for (int u = 0; u < SUB; ++u) {
-            uint32_t part[NPART][NT][2];
+        for (int u = 0; u < SUB; ++u)
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
                 float p[4];
@@ -413,20 +411,28 @@ template <int D, int NT> struct Mma {  // bf16: blocks of 8 NT heads
 #pragma unroll
                 for (int x = 0; x < NPART; ++x) {
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) part[x][j][i] = trans8(upper(p[2 * i], p[2 * i + 1]));
+                    for (int i = 0; i < 2; ++i) part[u][x][j][i] = trans8(upper(p[2 * i], p[2 * i + 1]));
 #pragma unroll
                     for (int i = 0; i < 4; ++i) p[i] -= __uint_as_float(__float_as_uint(p[i]) & 0xFFFF0000u);
                 }
             }
-            const uint32_t v = stage + P::HALF;
+        // A product's sum is cut, not rounded, where it is added to what was there, so the tile's sum
+        // starts from zero, its small parts first, and is added to o in fp32.
+        const uint32_t v = stage + P::HALF;
 #pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-                uint32_t a[4];
-                ldsm4t(a, v + P::at(u * 16 + row, 2 * k + c0));
+        for (int k = 0; k < D / 16; ++k) {
+            uint32_t a[SUB][4];
 #pragma unroll
-                for (int j = 0; j < NT; ++j)
+            for (int u = 0; u < SUB; ++u) ldsm4t(a[u], v + P::at(u * 16 + row, 2 * k + c0));
 #pragma unroll
-                    for (int x = 0; x < NPART; ++x) mma(o[k][j], a, part[x][j][0], part[x][j][1]);
+            for (int j = 0; j < NT; ++j) {
+                float c[4] = {};
+#pragma unroll
+                for (int x = NPART - 1; x >= 0; --x)
+#pragma unroll
+                    for (int u = 0; u < SUB; ++u) mma(c, a[u], part[u][x][j][0], part[u][x][j][1]);
+                o[k][j][0] = fma(o[k][j][0], f[j], mk(c[0], c[1]));
+                o[k][j][1] = fma(o[k][j][1], f[j], mk(c[2], c[3]));
             }
         }
     }
@@ -444,10 +450,13 @@ template <int D, int NT> struct Mma {  // bf16: blocks of 8 NT heads
                     sl[head] = l[j][i];
                 }
 #pragma unroll
-                for (int k = 0; k < D / 16; ++k) {
-                    so[head * D + slot_of(head, k * 16 + g)] = o[k][j][i];
-                    so[head * D + slot_of(head, k * 16 + g + 8)] = o[k][j][i + 2];
-                }
+                for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        float x[2];
+                        un(o[k][j][c], x[0], x[1]);
+                        so[head * D + slot_of(head, k * 16 + 8 * c + g)] = x[i];
+                    }
             }
     }
     static constexpr int EXTRA = 0;  // bytes of shared memory of the warp's own

@@ -43,3 +43,42 @@ def test_attn_decode_weights_keep_32_bits(dtype, d, Hq, Hk, tiles):
     worst = (np.abs(np64(o) - ref) / tol).max()
     assert worst <= 1, f"{worst} x tol"
     assert np.abs(np64(lse) - ref_lse).max() <= 2.0 ** -20 + (n / 16 + 8) * 2.0 ** -23
+
+
+@pytest.mark.parametrize("d,Hq", ((128, 3), (64, 12)))
+def test_attn_decode_long_sums_are_rounded_not_cut(d, Hq):
+    """A long sum of one sign, and at its end values that cancel it: what is left is the sum's error.
+
+    A warp adds up to 128 tiles.  Sums that are cut, not rounded, lose half a unit of the sum every
+    time: with 384 additions of a third of a tile's product 2^-17 of the whole.  Rounded to nearest, the
+    128 errors have no sign of their own: their standard deviation is 0.94 2^-23 of the whole for four
+    warps (a uniform error of the growing sum's last place each, the sum of 4 warps' variances), of which
+    six are allowed, 2^-20.5.  Besides: the weights' 2^-21.6 (score in base 2 off by 2^-23, the
+    exponential by 2^-22), what is cut inside a tile's three products, 3 x 2^-23 of the tile's sum, and
+    2^-22 for the last addition and the join."""
+    R, tiles = 300, 512
+    n, g = 16 * tiles, torch.Generator().manual_seed(d)
+    score = -torch.randint(0, 65, (n,), generator=g).double() / 64
+    score[::16] = 0.0
+    value = (1 + torch.randint(0, 128, (n, d), generator=g).double() / 128)
+    last = [n - 16, n - 13, n - 10]
+    score[last] = 0.0
+    value[last] = 0.0
+    p = score.exp()
+    left = (p[:, None] * value).sum(0)
+    whole = left.clone()
+    for t in last:
+        value[t] = -left.bfloat16().double()
+        left += value[t]
+    kc, vc = (torch.zeros(tiles, 16, 1, d, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    kc.view(n, d)[:, 0] = score.bfloat16().cuda()
+    vc.view(n, d).copy_(value.bfloat16())
+    q = torch.zeros(R, Hq, d, dtype=torch.bfloat16, device="cuda")
+    q[..., 0] = 1.0
+    table = torch.arange(tiles, dtype=torch.int32, device="cuda").expand(R, tiles).contiguous()
+    o, _ = binding.delta_rule_attn_decode(q, kc, vc, table, _i32([n] * R), scale=1.0)
+    torch.cuda.synchronize()
+    want = (left / p.sum()).numpy()
+    tol = (whole / p.sum()).numpy() * (2.0 ** -20.5 + 2.0 ** -21.6 + 3 * 2.0 ** -23 + 2.0 ** -22) + HALF["bf16"] * np.abs(want)
+    worst = (np.abs(np64(o) - want) / tol).max()
+    assert worst <= 1, f"{worst} x tol"
