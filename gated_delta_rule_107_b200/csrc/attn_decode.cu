@@ -34,10 +34,10 @@
 //     (with two, 2^-17 of p, outputs that are small against the values were off by more than fp32 sums
 //     are), and a tile's products are summed from zero and then added to o in fp32: the tensor cores
 //     cut what they add to a sum, and cutting the running sum a thousand times lost 2^-16 of it.  The
-//     additional products hide behind the loads, less so in wide groups (three requests of 200001
-//     tokens 186 -> 187 us, 64 of up to 16384 91.0 -> 91.5, one of 2000 7.5 -> 7.9; 32 of 6103 with
-//     groups of 16 29.8 -> 31.5, with 64 channels 21.8 -> 23.4).  Groups of 16 reach 79 to 83 % of the
-//     copy's rate, of 32 43 %.
+//     additional products hide behind the loads as long as several are in flight (three requests
+//     of 200001 tokens 183.3 us, as with two products into the running sum; with a kernel of 168
+//     registers and so fewer in flight 194), less so in wide groups (32 of 6103, groups of 16, 29.7 ->
+//     31.3).  Groups of 16 reach 79 to 83 % of the copy's rate, of 32 43 %.
 //   fp32.  CUDA cores, 1, 2, 4 or up to 8 heads at a time, packed arithmetic: a lane holds 4 channels
 //     of the heads' queries and outputs.  Groups of up to 4 are bound by the loads (87 to 94 % of the
 //     copy's rate), of 8 by two warps a scheduler working through their tiles (68 to 70 %).
@@ -102,10 +102,18 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-// the upper halves of two fp32 numbers: each one's first 8 bits as a bf16 number
-__device__ __forceinline__ uint32_t upper(float lo, float hi) {
-    return __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x7632);
+// 2^x for a weight or for a factor of what was summed before, not below the smallest normal number: an
+// infinite value that is seen makes its channel infinite, and a weight of zero would make 0 inf = NaN of
+// it.  Sums of finite values notice 2^-126 no more than they notice zero.  NaN stays.
+__device__ __forceinline__ float weight(float x) {
+    float y;
+    asm("max.NaN.f32 %0, %1, 0f00800000;" : "=f"(y) : "f"(ex2(x)));
+    return y;
 }
+// what is subtracted from scores: -inf minus -inf (nothing seen yet) would be NaN
+__device__ __forceinline__ float base_of(float m) { return m == -CUDART_INF_F ? 0.f : m; }
+// the sum of the weights: 0 where no score was above -inf (every weight is 2^-126 then); a NaN stays
+__device__ __forceinline__ float sum_of(float m, float l) { return m == -CUDART_INF_F && l == l ? 0.f : l; }
 
 // log of the sum l (base 2 maximum m); nothing seen: -inf; a NaN stays
 __device__ __forceinline__ float lse_of(float m, float l) { return l > 0.f ? (m + log2f(l)) * LN2 : (l == l ? -CUDART_INF_F : l); }
@@ -304,6 +312,8 @@ template <int D, int NT> struct Mma {  // bf16: blocks of 8 NT heads
     typedef __nv_bfloat16 E;
     static constexpr int GB = 8 * NT, STAGES = 3, CTAS = MAX_CTAS, SUB = 128 / D;  // 16 SUB tokens a tile
     static constexpr int NPART = 3;  // bf16 numbers that make up a weight: 8 bits each of its 24
+    static constexpr int KB = 4;     // blocks of 16 channels whose products are in flight at once
+    static_assert(D / 16 % KB == 0, "whole blocks");
     typedef Pipe<E, D, 16 * SUB, STAGES> P;
     uint32_t q[D / 16][NT][2], qn[D / 16][NT][2];
     f2 o[D / 16][NT][2];  // heads 2 t and 2 t + 1 of channel g, of channel g + 8
@@ -383,13 +393,15 @@ template <int D, int NT> struct Mma {  // bf16: blocks of 8 NT heads
                 mx[j][1] = fmaxf(mx[j][1], __shfl_xor_sync(0xffffffffu, mx[j][1], d));
             }
         f2 f[NT];
+        float from[NT][2];
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
             float fj[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const float mn = fmaxf(m[j][i], mx[j][i]);
-                fj[i] = m[j][i] == mn ? 1.f : ex2(m[j][i] - mn);  // equal: both may be -inf
+                from[j][i] = base_of(mn);
+                fj[i] = weight(m[j][i] - from[j][i]);
                 m[j][i] = mn;
                 l[j][i] *= fj[i];
             }
@@ -404,36 +416,51 @@ template <int D, int NT> struct Mma {  // bf16: blocks of 8 NT heads
                 float p[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    // -inf minus -inf (nothing seen yet) must not be NaN
-                    p[i] = s[u][j][i] == -CUDART_INF_F ? 0.f : ex2(s[u][j][i] - m[j][i & 1]);
+                    p[i] = weight(s[u][j][i] - from[j][i & 1]);
                     l[j][i & 1] += p[i];
                 }
+                // Each part but the last is the largest bf16 number below what is left, so that no part of
+                // a weight is zero or negative and an infinite value never meets one; the parts of weights
+                // below 2^-102 may have to be lifted to the smallest bf16 number, 2^-133.
 #pragma unroll
                 for (int x = 0; x < NPART; ++x) {
+                    int w[4];
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) part[u][x][j][i] = trans8(upper(p[2 * i], p[2 * i + 1]));
+                    for (int i = 0; i < 4; ++i) {
+                        const int b = __float_as_int(p[i]);
+                        w[i] = x == 0 ? b - 1 : (x < NPART - 1 ? __viaddmax_s32(b, -1, 0x10000) : max(b, 0x10000));
+                        p[i] -= __int_as_float(w[i] & 0xFFFF0000);
+                    }
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) p[i] -= __uint_as_float(__float_as_uint(p[i]) & 0xFFFF0000u);
+                    for (int i = 0; i < 2; ++i) part[u][x][j][i] = trans8(__byte_perm(w[2 * i], w[2 * i + 1], 0x7632));
                 }
             }
         // A product's sum is cut, not rounded, where it is added to what was there, so the tile's sum
         // starts from zero, its small parts first, and is added to o in fp32.
         const uint32_t v = stage + P::HALF;
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-            uint32_t a[SUB][4];
+        for (int k0 = 0; k0 < D / 16; k0 += KB) {
+            uint32_t a[KB][SUB][4];
+            float c[KB][NT][4] = {};
 #pragma unroll
-            for (int u = 0; u < SUB; ++u) ldsm4t(a[u], v + P::at(u * 16 + row, 2 * k + c0));
+            for (int k = 0; k < KB; ++k)
 #pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                float c[4] = {};
+                for (int u = 0; u < SUB; ++u) ldsm4t(a[k][u], v + P::at(u * 16 + row, 2 * (k0 + k) + c0));
 #pragma unroll
-                for (int x = NPART - 1; x >= 0; --x)
+            for (int x = NPART - 1; x >= 0; --x)
 #pragma unroll
-                    for (int u = 0; u < SUB; ++u) mma(c, a[u], part[u][x][j][0], part[u][x][j][1]);
-                o[k][j][0] = fma(o[k][j][0], f[j], mk(c[0], c[1]));
-                o[k][j][1] = fma(o[k][j][1], f[j], mk(c[2], c[3]));
-            }
+                for (int u = 0; u < SUB; ++u)
+#pragma unroll
+                    for (int k = 0; k < KB; ++k)
+#pragma unroll
+                        for (int j = 0; j < NT; ++j) mma(c[k][j], a[k][u], part[u][x][j][0], part[u][x][j][1]);
+#pragma unroll
+            for (int k = 0; k < KB; ++k)
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+                    o[k0 + k][j][0] = fma(o[k0 + k][j][0], f[j], mk(c[k][j][0], c[k][j][1]));
+                    o[k0 + k][j][1] = fma(o[k0 + k][j][1], f[j], mk(c[k][j][2], c[k][j][3]));
+                }
         }
     }
     __device__ __forceinline__ void finish(float *sm, float *sl, float *so) {
@@ -447,7 +474,7 @@ template <int D, int NT> struct Mma {  // bf16: blocks of 8 NT heads
                 const int head = j * 8 + 2 * t + i;
                 if (g == 0) {
                     sm[head] = m[j][i];
-                    sl[head] = l[j][i];
+                    sl[head] = sum_of(m[j][i], l[j][i]);
                 }
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k)
@@ -553,10 +580,9 @@ template <int D, int H> struct Simt {
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             const float mn = fmaxf(m[c], mx[c]);
-            const float f = m[c] == mn ? 1.f : ex2(m[c] - mn);  // equal: both may be -inf
+            const float f = weight(m[c] - base_of(mn)), p = weight(s[c] - base_of(mn));
             up = up || m[c] != mn;
             m[c] = mn;
-            const float p = s[c] == -CUDART_INF_F ? 0.f : ex2(s[c] - mn);  // -inf minus -inf must not be NaN
             l[c] = l[c] * f + p;
             if (first()) {
                 ps[t * GB + h0 + c] = mk(p, p);
@@ -601,7 +627,7 @@ template <int D, int H> struct Simt {
             for (int d = LT; d < 32; d <<= 1) l[c] += __shfl_xor_sync(0xffffffffu, l[c], d);
             if (first() && token() == 0) {
                 sm[head() + c] = m[c];
-                sl[head() + c] = l[c];
+                sl[head() + c] = sum_of(m[c], l[c]);
             }
         }
 #pragma unroll
@@ -621,7 +647,7 @@ template <int D, int H> struct Simt {
 template <class C, int D> constexpr int warp_bytes() { return C::STAGES * C::P::STAGE + C::EXTRA; }
 template <class C, int D> constexpr int smem_bytes() { return WARPS * warp_bytes<C, D>(); }
 
-template <class C, int D> __global__ void __launch_bounds__(THREADS) k_attn(const Args x) {
+template <class C, int D> __global__ void __launch_bounds__(THREADS, MAX_CTAS / 148) k_attn(const Args x) {
     typedef typename C::E E;
     typedef typename C::P P;
     constexpr int GB = C::GB, STAGES = C::STAGES, TILE = P::TILE;
@@ -731,7 +757,7 @@ template <class C, int D> __global__ void __launch_bounds__(THREADS) k_attn(cons
             for (int w = 1; w < WARPS; ++w) mx = fmaxf(mx, sm_m[w][hd]);
 #pragma unroll
             for (int w = 0; w < WARPS; ++w) {
-                const float l = sm_l[w][hd], f = l == 0.f ? 0.f : ex2(sm_m[w][hd] - mx);  // l = 0: m may be -inf
+                const float l = sm_l[w][hd], f = l == 0.f ? 0.f : weight(sm_m[w][hd] - mx);  // l = 0: m may be -inf
                 s += l * f;
                 const float4 *p = reinterpret_cast<const float4 *>(smem + sm_at[w]) + (hd * D + slot_of(hd, ch)) / 4;
                 const float4 u = p[0], v = p[1];
@@ -795,7 +821,7 @@ template <typename E, int D> __global__ void __launch_bounds__(256) k_attn_join(
 #pragma unroll
             for (int u = 0; u < 4; ++u)
                 if (i + u * step < n) mb = fmaxf(mb, ml[u].x);
-            const float g = m == mb ? 1.f : ex2(m - mb);  // equal: both may be -inf
+            const float g = m == mb ? 1.f : weight(m - mb);  // equal: both may be -inf
             m = mb;
             l *= g;
 #pragma unroll
@@ -803,7 +829,7 @@ template <typename E, int D> __global__ void __launch_bounds__(256) k_attn_join(
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
                 if (i + u * step >= n) break;
-                const float f = ml[u].y == 0.f ? 0.f : ex2(ml[u].x - m);  // l = 0: the part's m may be -inf
+                const float f = ml[u].y == 0.f ? 0.f : weight(ml[u].x - m);  // l = 0: the part's m may be -inf
                 l += ml[u].y * f;
 #pragma unroll
                 for (int c = 0; c < NC; ++c) o[c] += f * y[u][c];
@@ -828,7 +854,7 @@ template <typename E, int D> __global__ void __launch_bounds__(256) k_attn_join(
             l = 0.f;
 #pragma unroll
             for (int w = 0; w < JW; ++w) {
-                g[w] = wl[w] == 0.f ? 0.f : ex2(wm[w] - m);
+                g[w] = wl[w] == 0.f ? 0.f : weight(wm[w] - m);
                 l += wl[w] * g[w];
             }
             for (int c = threadIdx.x; c < D; c += JW * 32) {

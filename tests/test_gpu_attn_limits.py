@@ -82,3 +82,62 @@ def test_attn_decode_long_sums_are_rounded_not_cut(d, Hq):
     tol = (whole / p.sum()).numpy() * (2.0 ** -20.5 + 2.0 ** -21.6 + 3 * 2.0 ** -23 + 2.0 ** -22) + HALF["bf16"] * np.abs(want)
     worst = (np.abs(np64(o) - want) / tol).max()
     assert worst <= 1, f"{worst} x tol"
+
+
+@pytest.mark.parametrize("dtype", ("f32", "bf16"))
+@pytest.mark.parametrize("d,Hq,Hk", ((64, 2, 1), (128, 3, 1), (128, 12, 1), (64, 32, 2), (128, 8, 8)))
+def test_attn_decode_visible_infinities(dtype, d, Hq, Hk):
+    """A value that is infinite and seen makes its channel infinite, whatever its weight; both signs
+    together make NaN; other channels, heads and requests keep their numbers."""
+    inf = float("inf")
+    lens = [1, 3000, 3000, 700, 40]
+    page, width = 16, 188
+    g = torch.Generator().manual_seed(d + Hq)
+    P = len(lens) * width
+    kc, vc = (torch.randn(P, page, Hk, d, generator=g).to(DT[dtype]).cuda() for _ in range(2))
+    q = torch.randn(len(lens), Hq, d, generator=g).to(DT[dtype]).cuda()
+    table = torch.arange(P, dtype=torch.int32, device="cuda").view(len(lens), width)
+    lens_t = _i32(lens)
+    plain, lse = binding.delta_rule_attn_decode(q, kc, vc, table, lens_t, want_lse=True)
+    want = plain.clone()
+
+    def put(r, t, h, ch, x):
+        vc[table[r, t // page], t % page, h, ch] = x
+        heads = slice(h * (Hq // Hk), (h + 1) * (Hq // Hk))
+        want[r, heads, ch] = torch.where(want[r, heads, ch] == -x, torch.full_like(want[r, heads, ch], float("nan")),
+                                         torch.full_like(want[r, heads, ch], x))
+
+    put(0, 0, 0, 3, inf)                       # one token: its weight is 1
+    put(0, 0, Hk - 1, d - 1, -inf)
+    for t in (0, 1, 17, 1500, 2999):           # weights with a rest of either sign; early ones are scaled down later
+        put(1, t, 0, (5 * t) % d, inf)
+    put(2, 100, 0, 7, inf)                     # both signs: NaN
+    put(2, 2500, 0, 7, -inf)
+    put(3, 699, Hk - 1, 0, -inf)
+    vc[table[4, 2], 8, 0, 5] = inf             # token 40: not seen
+    o, lse2 = binding.delta_rule_attn_decode(q, kc, vc, table, lens_t, want_lse=True)
+    torch.cuda.synchronize()
+    assert torch.equal(lse, lse2)
+    assert torch.equal(o.isnan(), want.isnan()) and torch.equal(o.nan_to_num(nan=0.0), want.nan_to_num(nan=0.0))
+
+
+@pytest.mark.parametrize("dtype", ("f32", "bf16"))
+def test_attn_decode_infinity_of_no_noticeable_weight(dtype):
+    """An infinite value whose score lies 300 below the largest, seen before it, after it and beside it."""
+    d, n = 64, 2000
+    kc, vc = (torch.zeros(n // 16, 16, 1, d, dtype=DT[dtype], device="cuda") for _ in range(2))
+    q = torch.zeros(1, 2, d, dtype=DT[dtype], device="cuda")
+    q[..., 0] = 1.0
+    vc[:] = 0.5
+    k = kc.view(n, d)
+    table = torch.arange(n // 16, dtype=torch.int32, device="cuda")[None]
+    for top in (0, 3, 1000, n - 1):
+        k[:, 0] = -300.0
+        k[top, 0] = 0.0
+        for t in (1, 2, 14, 999, 1001, n - 2):
+            vc.view(n, d)[t, 9] = float("inf")
+            o, lse = binding.delta_rule_attn_decode(q, kc, vc, table, _i32([n]), scale=1.0, want_lse=True)
+            torch.cuda.synchronize()
+            vc.view(n, d)[t, 9] = 0.5
+            assert (o[..., 9] == float("inf")).all(), (top, t)
+            assert (o[..., :9] == 0.5).all() and (lse.abs() <= 2.0 ** -21).all(), (top, t)
