@@ -152,15 +152,19 @@ template <int UNROLL> __global__ void __launch_bounds__(MAX_THREADS) k_pages(con
 cudaError_t pages_run(const Pages &args, cudaStream_t s) {
     Pages p = args;
     p.by_page = FastDiv(p.page);
-    const size_t smem = (3 * (size_t)p.R + 2) * sizeof(int);
+    auto bytes = [](int R) { return (3 * (size_t)R + 2) * sizeof(int); };
+    const size_t smem = bytes(p.R);
     // One token a lane in CTAs of 256 threads while one wave of them holds all tokens (66 tokens of 64
     // requests: 3.1 us, four a lane 5.1), else eight a lane, whose reads overlap and whose search is
     // shared, in CTAs of 1024, so that the prefix sums are formed once an SM (10^6 tokens of 509
     // requests: 7.9 us, four a lane 9.4, one a lane 15.3).  The requests' own outputs need a thread each as well.
     const long long most = p.N > p.R ? p.N : p.R;
     auto go = [&](auto kern, int threads, int unroll) -> cudaError_t {
-        if (smem > 48 * 1024) {
-            const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        // Without this a launch has 48 KB, the kernel's static part among them.  The most that any call
+        // needs, whatever this one does: another thread's launch may come between.
+        if (smem > 32 * 1024) {
+            const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                       (int)bytes(PAGES_MAX_REQUESTS));
             if (e != cudaSuccess) return e;
         }
         long long ctas = (most + threads * unroll - 1) / (threads * unroll);

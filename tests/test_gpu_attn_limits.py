@@ -141,3 +141,41 @@ def test_attn_decode_infinity_of_no_noticeable_weight(dtype):
             vc.view(n, d)[t, 9] = 0.5
             assert (o[..., 9] == float("inf")).all(), (top, t)
             assert (o[..., :9] == 0.5).all() and (lse.abs() <= 2.0 ** -21).all(), (top, t)
+
+
+# ------------------------------------------------------------------------------------ pages
+SIZES = """
+import sys
+import torch
+from gated_delta_rule_107_b200 import binding
+from oracle import attn as oa
+each = int(sys.argv[1])
+for R in (4074, 4075, 4090, 4095, 4096):
+    cached = torch.arange(R, dtype=torch.int32) % 5
+    fresh = torch.full((R,), each, dtype=torch.int32)
+    fresh[::3] = 0
+    page, N = 4, int(fresh.sum()) + 3
+    width = (4 + each) // page + 1
+    table = torch.full((R, width), -1, dtype=torch.int32)
+    table[:, :2] = torch.arange(2 * R, dtype=torch.int32).view(R, 2)
+    free = torch.arange(R * width, dtype=torch.int32) + 2 * R
+    want = oa.pages(cached.numpy(), fresh.numpy(), free.numpy(), len(free), table.numpy(), page, N)
+    t = table.cuda()
+    got = binding.delta_rule_pages(cached.cuda(), fresh.cuda(), free.cuda(),
+                                   torch.tensor([len(free)], dtype=torch.int32, device="cuda"), t, page, N) + (t,)
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert (a.cpu().long() == torch.as_tensor(b).long()).all(), R
+"""
+
+
+@pytest.mark.parametrize("each", (1, 16))
+def test_pages_of_thousands_of_requests_in_a_fresh_process(each):
+    """Prefix sums around the shared memory that a kernel has unasked, with no larger call before them;
+    few tokens, and so many that a lane takes several."""
+    import subprocess
+    import sys
+
+    from conftest import ROOT
+    r = subprocess.run([sys.executable, "-c", SIZES, str(each)], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
