@@ -124,8 +124,8 @@ struct Span {
     template <int TILE> __device__ __forceinline__ void set(const AttnDecode &a, int r) {
         const long long room = (long long)a.width * a.page;
         n = max(a.lens[r], 0);
+        first = a.window > 0 && n > a.window ? n - a.window : 0;  // counts back from the length, which may lie behind the table
         if (n > room) n = (int)room;
-        first = a.window > 0 && n > a.window ? n - a.window : 0;
         tile0 = first / TILE;
         tiles = n > first ? (n - 1) / TILE - tile0 + 1 : 0;
     }

@@ -87,8 +87,11 @@ def attn_decode(q, k_cache, v_cache, table, lens, scale=None, window=0):
     scale = d ** -0.5 if scale is None else scale
     o, lse = np.zeros((R, Hq, d)), np.full((R, Hq), -np.inf)
     for r in range(R):
-        n = min(max(int(lens[r]), 0), table.shape[1] * page)
+        # the window counts back from the length; beyond room + window it sees nothing of the table
+        room = table.shape[1] * page
+        n = min(max(int(lens[r]), 0), room + window)
         t = np.arange(max(0, n - window) if window else 0, n)
+        t = t[t < room]
         pg = np.asarray(table[r])[t // page] if n else t
         ok = (pg >= 0) & (pg < n_pages)
         t, pg = t[ok], pg[ok]

@@ -179,3 +179,29 @@ def test_pages_of_thousands_of_requests_in_a_fresh_process(each):
     from conftest import ROOT
     r = subprocess.run([sys.executable, "-c", SIZES, str(each)], cwd=ROOT, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("dtype", ("f32", "bf16"))
+@pytest.mark.parametrize("told,window,seen", ((74, 16, range(58, 64)), (80, 16, ()), (79, 16, (63,)), (2 ** 31 - 1, 2 ** 31 - 60, range(59, 64)),
+                                              (2 ** 31 - 1, 5, ()), (64, 16, range(48, 64)), (100, 0, range(64))))
+def test_attn_decode_window_counts_back_from_the_length(dtype, told, window, seen):
+    """A length behind the table: of the window's tokens only those inside it are seen."""
+    g = torch.Generator().manual_seed(1)
+    kc, vc = (torch.randn(5, 16, 1, 64, generator=g).to(DT[dtype]).cuda() for _ in range(2))
+    q = torch.randn(2, 2, 64, generator=g).to(DT[dtype]).cuda()
+    table = _i32([[3, 0, 4, 1], [2, 1, 0, 3]])
+    o, lse = binding.delta_rule_attn_decode(q, kc, vc, table, _i32([told, 20]), window=window, want_lse=True)
+    torch.cuda.synchronize()
+    seen = list(seen)
+    if not seen:
+        assert (o[0] == 0).all() and torch.isneginf(lse[0]).all()
+        return
+    k, v = (np64(c)[[3, 0, 4, 1]].reshape(64, 64)[seen] for c in (kc, vc))
+    s = np64(q)[0] @ k.T / 8
+    p = np.exp(s - s.max(-1, keepdims=True))
+    want = p @ v / p.sum(-1, keepdims=True)
+    # scores of 64 products in 32 bits, weights, sums: far below what a token more or less changes
+    ds = 68 * 2.0 ** -23 * (np.abs(np64(q)[0]) @ np.abs(k).T).max() / 8
+    tol = HALF[dtype] * np.abs(want) + np.abs(v).max() * (2 * ds + 2.0 ** -20 + 72 * 2.0 ** -23)
+    assert (np.abs(np64(o)[0] - want) <= tol).all()
+    assert np.abs(np64(lse)[0] - (s.max(-1) + np.log(p.sum(-1)))).max() <= ds + 2.0 ** -20 + 72 * 2.0 ** -23
