@@ -23,6 +23,7 @@
 // all issue slots were taken), and neighbouring lanes always hold neighbouring vectors (with the
 // channels behind rot two vectors a lane side by side, 32768 tokens with half of the channels
 // rotated took 118 us backward instead of 86).
+#include <cfloat>
 #include <type_traits>
 
 #include "qkrope.cuh"
@@ -44,7 +45,7 @@ using namespace dr::f32x2;
 // chosen so that the two channels of each pair meet in the lane, as VEC first and VEC second
 // channels of pairs, two to a register pair: channels i of the vectors a and b (pairs (i, i + rot/2)),
 // or the even and the odd channels of both (interleaved).  Channels behind rot are held alike and
-// turned by nothing.
+// not turned.
 template <typename E, int D, bool INTER> struct Lay {
     static constexpr int VEC = 16 / (int)sizeof(E), N2 = VEC / 2, LPT = D / (2 * VEC), TPW = 32 / LPT;
     int j, ia, ib;
@@ -295,7 +296,8 @@ __global__ void __launch_bounds__(THREADS, 3) k_qkrope(const QkRope p, int hpg) 
             for (int h = from; h < to; ++h, dst += apart) {
                 f2 A[N2], B[N2], ss = 0;
                 ring.wait();
-                open<INTER>(lds16(ring.got), lds16(ring.got + ring.VECTOR), A, B, (E *)nullptr);
+                const uint32_t at = ring.got;
+                open<INTER>(lds16(at), lds16(at + ring.VECTOR), A, B, (E *)nullptr);
                 push();
                 ring.popped();
 #pragma unroll
@@ -306,7 +308,19 @@ __global__ void __launch_bounds__(THREADS, 3) k_qkrope(const QkRope p, int hpg) 
                     B[i] = mul(B[i], wB[i]);
                 }
                 rotate<N2, false>(A, B, cs, sn);
-                const float r = rsqrtf(sum_group<LPT>(sum2(ss)) * (1.f / D) + EPS);
+                const float mean = sum_group<LPT>(sum2(ss)) * (1.f / D), r = rsqrtf(mean + EPS);
+                if (!(mean <= FLT_MAX) && !l.turned) {
+                    // A turn by nothing makes NaN of the channel beside an infinite one: the row's values as
+                    // they were (its slot is filled again by the next push).  Behind the sum, so that the
+                    // turn still runs beside it (8192 tokens of 20 heads: 14.0 -> 14.4 us; with the branch
+                    // around the turn 15.4).
+                    open<INTER>(lds16(at), lds16(at + ring.VECTOR), A, B, (E *)nullptr);
+#pragma unroll
+                    for (int i = 0; i < N2; ++i) {
+                        A[i] = mul(A[i], wA[i]);
+                        B[i] = mul(B[i], wB[i]);
+                    }
+                }
                 const f2 rr = mk(r, r);
 #pragma unroll
                 for (int i = 0; i < N2; ++i) {
@@ -433,7 +447,7 @@ __global__ void __launch_bounds__(THREADS, 2) k_qkrope_bwd(const QkRope p, long 
                 open<INTER>(lds16(ring.got), lds16(ring.got + ring.VECTOR), A, B, (E *)nullptr);
                 push();
                 ring.popped();
-                rotate<N2, true>(gA, gB, cs, sn);
+                if (l.turned) rotate<N2, true>(gA, gB, cs, sn);  // a turn by nothing: see k_qkrope
 #pragma unroll
                 for (int i = 0; i < N2; ++i) {
                     ss = fma(A[i], A[i], ss);

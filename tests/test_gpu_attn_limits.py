@@ -205,3 +205,30 @@ def test_attn_decode_window_counts_back_from_the_length(dtype, told, window, see
     tol = HALF[dtype] * np.abs(want) + np.abs(v).max() * (2 * ds + 2.0 ** -20 + 72 * 2.0 ** -23)
     assert (np.abs(np64(o)[0] - want) <= tol).all()
     assert np.abs(np64(lse)[0] - (s.max(-1) + np.log(p.sum(-1)))).max() <= ds + 2.0 ** -20 + 72 * 2.0 ** -23
+
+
+# ------------------------------------------------------------------------------------ norm and rotation
+@pytest.mark.parametrize("dtype", ("f32", "bf16"))
+@pytest.mark.parametrize("interleaved", (False, True))
+@pytest.mark.parametrize("d,rot", ((64, 0), (128, 64), (128, 96), (64, 16)))
+def test_qkrope_infinity_in_a_channel_that_is_not_turned(dtype, interleaved, d, rot):
+    """It stays in its channel: the row's others are divided by an infinite norm, and in the backward the
+    weights' gradients of other channels are finite."""
+    g = torch.Generator().manual_seed(d + rot)
+    N = 8
+    f = 100.0 ** (-torch.arange(0, rot, 2, dtype=torch.float64) / d).cuda() if rot else None
+    for c in (rot, rot + 5, d - 1, (rot + d) // 2):
+        x, dy = (torch.randn(N, 2, d, generator=g).to(DT[dtype]).cuda() for _ in range(2))
+        others = torch.arange(d, device="cuda") != c
+        y = x.clone()
+        y[3, 1, c] = float("inf")
+        out, _ = binding.delta_rule_qkrope(y, x, None, None, f, interleaved=interleaved)
+        plain, _ = binding.delta_rule_qkrope(x, x, None, None, f, interleaved=interleaved)
+        dy2 = dy.clone()
+        dy2[3, 1, c] = float("inf")
+        dw = binding.delta_rule_qkrope_bwd(x, x, None, None, f, dy2, dy, interleaved=interleaved)[2:]
+        torch.cuda.synchronize()
+        assert (out[3, 1, others] == 0).all() and out[3, 1, c].isnan()
+        plain[3, 1] = out[3, 1]
+        assert torch.equal(out[:, :, others], plain[:, :, others])
+        assert torch.equal(dw[0][others], dw[1][others]) and dw[0][c] == float("inf") * x[3, 1, c].item() and dw[1].isfinite().all()
