@@ -376,6 +376,8 @@ template <int TPW> struct Items {
     }
 };
 
+__device__ const uint4 no_row[32] = {};  // a row of zeros of the largest type and size
+
 // part (or null): [CTA][2][D], the CTA's sums of the weights' gradients (query, key)
 template <typename E, int D, bool INTER>
 __global__ void __launch_bounds__(THREADS, 2) k_qkrope_bwd(const QkRope p, long long per) {
@@ -394,7 +396,7 @@ __global__ void __launch_bounds__(THREADS, 2) k_qkrope_bwd(const QkRope p, long 
     const unsigned N = (unsigned)p.N;
     auto token = [&](unsigned at) { return (size_t)min(at + lane / LPT, N - 1); };
     Items<TPW> next = now;
-    int left = 0;
+    int left = 0, apart = D;
     const E *src = nullptr, *grad = nullptr;
     auto push = [&]() {
         if (next.todo > 0) {
@@ -410,6 +412,10 @@ __global__ void __launch_bounds__(THREADS, 2) k_qkrope_bwd(const QkRope p, long 
                     grad = (const E *)p.gk + (n * p.Hk + h - p.Hq) * D;
                     left = next.heads - h;
                 }
+                if (next.tok + lane / LPT >= N) {  // behind the last token: rows of zeros, which add nothing to dw
+                    src = grad = reinterpret_cast<const E *>(no_row);
+                    apart = 0;
+                }
                 next.head += left;
                 if (next.head == next.heads) {
                     next.head = 0;
@@ -420,8 +426,8 @@ __global__ void __launch_bounds__(THREADS, 2) k_qkrope_bwd(const QkRope p, long 
             cp16(ring.put + ring.VECTOR, src + l.ib * VEC);
             cp16(ring.put + 2 * ring.VECTOR, grad + l.ia * VEC);
             cp16(ring.put + 3 * ring.VECTOR, grad + l.ib * VEC);
-            src += D;
-            grad += D;
+            src += apart;
+            grad += apart;
             --left;
             --next.todo;
         }
@@ -454,8 +460,7 @@ __global__ void __launch_bounds__(THREADS, 2) k_qkrope_bwd(const QkRope p, long 
                     ss = fma(B[i], B[i], ss);
                 }
                 const float r = rsqrtf(sum_group<LPT>(sum2(ss)) * (1.f / D) + EPS);
-                const float rl = act ? r : 0.f;  // a group behind the last token adds nothing
-                const f2 rr = mk(rl, rl);
+                const f2 rr = mk(r, r);
                 f2 wA[N2], wB[N2];
                 sh.weights(which, j, wA, wB);
 #pragma unroll

@@ -232,3 +232,19 @@ def test_qkrope_infinity_in_a_channel_that_is_not_turned(dtype, interleaved, d, 
         plain[3, 1] = out[3, 1]
         assert torch.equal(out[:, :, others], plain[:, :, others])
         assert torch.equal(dw[0][others], dw[1][others]) and dw[0][c] == float("inf") * x[3, 1, c].item() and dw[1].isfinite().all()
+
+
+@pytest.mark.parametrize("dtype", ("f32", "bf16"))
+@pytest.mark.parametrize("N,d", ((1, 64), (5, 128), (9, 64)))
+def test_qkrope_infinite_gradient_of_the_last_token(dtype, N, d):
+    """Lanes behind the last token add nothing to the weights' gradients, whatever the last one's gradient is."""
+    g = torch.Generator().manual_seed(N)
+    x = torch.randn(N, 2, d, generator=g).to(DT[dtype]).cuda()
+    dy = torch.randn(N, 2, d, generator=g).to(DT[dtype]).cuda()
+    dy[-1, 1, 3] = float("inf")
+    dw = binding.delta_rule_qkrope_bwd(x, x, None, None, None, dy, dy)[2:]
+    torch.cuda.synchronize()
+    want = dw[0].cpu().clone()
+    want[3] = float("inf") * x[-1, 1, 3].item()  # the definition: the sum over rows of dy n
+    for w in dw:
+        assert w[torch.arange(d) != 3].isfinite().all() and torch.equal(w.cpu(), want)
