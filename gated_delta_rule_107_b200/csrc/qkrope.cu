@@ -160,10 +160,13 @@ template <typename E, int D, bool INTER> struct Shared {
             B[2 * i] = mk(v.x, v.y); B[2 * i + 1] = mk(v.z, v.w);
         }
     }
-    // cosines and sines of a lane's angles.  fp32 results take sincospif (2 ulp); for bf16 the fast
-    // sine and cosine, off by less than 2^-20 here, are a 4096th of a rounding and a few instructions
-    // instead of some forty.
-    __device__ __forceinline__ void angles(int pos, int j, f2 *cs, f2 *sn) const {
+    // Cosines and sines of a lane's angles.  fp32 results, the weights' gradients of every type among
+    // them, take sincospif (2 ulp; backward 45.7 -> 46.0 us at 8 x 4096).  Where all results are bf16
+    // (FAST) the fast sine and cosine serve, off by less than 2^-20 here: a 4096th of the rounding of the
+    // pair's larger channel, and a few instructions instead of some forty (8 x 4096 tokens 30.6 us instead
+    // of 31.1, 8192 into the cache 14.5 instead of 15.1; a series of eleven terms in packed arithmetic 31.1
+    // and 15.8).
+    template <bool FAST> __device__ __forceinline__ void angles(int pos, int j, f2 *cs, f2 *sn) const {
         const double p = (double)pos;
 #pragma unroll
         for (int i = 0; i < VEC; i += 2) {
@@ -172,11 +175,11 @@ template <typename E, int D, bool INTER> struct Shared {
             for (int k = 0; k < 2; ++k) {
                 const double t = p * turns[i + k][j];
                 const float f = (float)(t - rint(t));
-                if (sizeof(E) == 4) {
-                    sincospif(2.f * f, &s[k], &c[k]);
-                } else {
+                if (FAST) {
                     s[k] = __sinf(6.28318530717958647692f * f);
                     c[k] = __cosf(6.28318530717958647692f * f);
+                } else {
+                    sincospif(2.f * f, &s[k], &c[k]);
                 }
             }
             cs[i / 2] = mk(c[0], c[1]);
@@ -284,7 +287,7 @@ __global__ void __launch_bounds__(THREADS, 3) k_qkrope(const QkRope p, int hpg) 
         const bool act = n0 + lane / LPT < N;
         const size_t n = token(n0);
         f2 cs[N2], sn[N2];
-        sh.angles(p.pos ? p.pos[n] : (int)((unsigned)n % (unsigned)p.T), j, cs, sn);
+        sh.template angles<sizeof(E) == 2>(p.pos ? p.pos[n] : (int)((unsigned)n % (unsigned)p.T), j, cs, sn);
         // heads [from, to) of one tensor, to dst, `apart` from head to head
         auto run = [&](E *dst, long long apart, int which, int from, int to) {
             if (from >= to) return;
@@ -442,7 +445,7 @@ __global__ void __launch_bounds__(THREADS, 2) k_qkrope_bwd(const QkRope p, long 
         const size_t n = token(now.tok);
         const int h0 = now.head, h1 = min(now.heads, h0 + now.todo);
         f2 cs[N2], sn[N2];
-        sh.angles(p.pos ? p.pos[n] : (int)((unsigned)n % (unsigned)p.T), j, cs, sn);
+        sh.template angles<false>(p.pos ? p.pos[n] : (int)((unsigned)n % (unsigned)p.T), j, cs, sn);
         auto run = [&](E *dst, int which, f2 *dw, int from, int to) {
             dst += from * D;
 #pragma unroll 1

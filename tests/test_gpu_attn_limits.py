@@ -248,3 +248,29 @@ def test_qkrope_infinite_gradient_of_the_last_token(dtype, N, d):
     want[3] = float("inf") * x[-1, 1, 3].item()  # the definition: the sum over rows of dy n
     for w in dw:
         assert w[torch.arange(d) != 3].isfinite().all() and torch.equal(w.cpu(), want)
+
+
+@pytest.mark.parametrize("dtype,interleaved", (("f32", False), ("bf16", False), ("bf16", True)))
+def test_qkrope_angles_keep_32_bits(dtype, interleaved):
+    """The weights' gradients are fp32 whatever the inputs' type: for one row with the gradient 1 in the
+    first channel of every pair they are n cos(angle) there and -n sin(angle) in the second.
+
+    Rows of ones, so that n is one number, which position 0 gives as the kernel has it.  The angle's
+    fraction of a turn is rounded once in [-1/2, 1/2], 2^-26 turns or 2^-23.3; a cosine to 32 bits is off
+    by 2 units of 2^-24 more, the product by 2^-24 of itself: 2^-22 covers them."""
+    d = 128
+    x = torch.ones(1, 1, d, dtype=DT[dtype], device="cuda")
+    ia, ib = (torch.arange(0, d, 2), torch.arange(1, d, 2)) if interleaved else (torch.arange(d // 2), torch.arange(d // 2, d))
+    dy = torch.zeros_like(x)
+    dy[0, 0, ia.cuda()] = 1.0
+    f = 10000.0 ** (-torch.arange(0, d, 2, dtype=torch.float64) / d)
+    pos = torch.tensor([0, 1, 2, 3, 5, 7, 50, 999] + [1000 + 37 * i for i in range(120)], dtype=torch.int32)
+    got = torch.stack([binding.delta_rule_qkrope_bwd(x, x, None, None, f.cuda(), dy, dy, p.cuda().view(1), interleaved)[2]
+                       for p in pos])
+    torch.cuda.synchronize()
+    got = got.cpu().double()
+    n = got[0, ia[0]]
+    angle = pos.double()[:, None] * f
+    worst = max((got[:, ia] / n - angle.cos()).abs().max().item(), (got[:, ib] / n + angle.sin()).abs().max().item())
+    assert abs(n - 1 / (1 + 1e-6) ** 0.5) <= 2.0 ** -22
+    assert worst <= 2.0 ** -22, f"off by {worst * 2 ** 22} x 2^-22"
