@@ -191,9 +191,19 @@ PyObject *pages(PyObject *, Args a, Py_ssize_t n) {
          *tp = dense(table, "table", at::kInt, dev, -1);
     if (R > 8192 || N > 1 << 30) return code(DR_ERR_UNSUPPORTED);  // before gigabytes are allocated for the refusal
     On on(dev);
-    Together t(12ll * N + 8ll * R + 8, dev);  // the 8-byte elements first
-    const at::Tensor slots = t.next(at::kLong, {N}), pos = t.next(at::kInt, {N}), lens = t.next(at::kInt, {R}),
-                     cu = t.next(at::kInt, {R + 1ll}), left = t.next(at::kInt, {1});
+    // lens and n_left are kept for the next step, the rows' outputs are not: those of many tokens stand alone
+    const bool apart = 12ll * N > SMALL;
+    at::Tensor slots, pos;
+    if (apart) {
+        slots = empty({N}, at::kLong, dev);
+        pos = empty({N}, at::kInt, dev);
+    }
+    Together t((apart ? 0 : 12ll * N) + 8ll * R + 8, dev);  // the 8-byte elements first
+    if (!apart) {
+        slots = t.next(at::kLong, {N});
+        pos = t.next(at::kInt, {N});
+    }
+    const at::Tensor lens = t.next(at::kInt, {R}), cu = t.next(at::kInt, {R + 1ll}), left = t.next(at::kInt, {1});
     const int rc = c_pages((int *)cp, (int *)fp, (int *)sp, (int *)np, (int *)tp, (int *)lens.data_ptr(), (int *)cu.data_ptr(),
                            (int *)pos.data_ptr(), (long long *)slots.data_ptr(), (int *)left.data_ptr(), R,
                            extent(stack.numel(), "free_pages"), extent(table.size(1), "table"), page, N, on.stream);

@@ -274,3 +274,18 @@ def test_qkrope_angles_keep_32_bits(dtype, interleaved):
     worst = max((got[:, ia] / n - angle.cos()).abs().max().item(), (got[:, ib] / n + angle.sin()).abs().max().item())
     assert abs(n - 1 / (1 + 1e-6) ** 0.5) <= 2.0 ** -22
     assert worst <= 2.0 ** -22, f"off by {worst * 2 ** 22} x 2^-22"
+
+
+def test_pages_small_outputs_do_not_hold_the_large_ones():
+    """n_left and lens are kept for the next step; the positions and slots of a large prefill are not."""
+    R, N = 40, 300000
+    cached, fresh = _i32([0] * R), _i32([N // R] * R)
+    table = torch.full((R, N // R // 64 + 1), -1, dtype=torch.int32, device="cuda")
+    free = torch.arange(table.numel(), dtype=torch.int32, device="cuda")
+    lens, cu, pos, slots, left = binding.delta_rule_pages(cached, fresh, free, _i32([free.numel()]), table, 64, N)
+    torch.cuda.synchronize()
+    assert left.item() == free.numel() - R * -(-(N // R) // 64) and slots.numel() == pos.numel() == N
+    for t in (lens, cu, left):
+        assert t.untyped_storage().nbytes() <= 8 * R + 64
+    few = binding.delta_rule_pages(cached, fresh, free, _i32([free.numel()]), table, 64, 100)  # all in one piece
+    assert len({t.untyped_storage().data_ptr() for t in few}) == 1
