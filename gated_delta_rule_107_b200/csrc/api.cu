@@ -850,6 +850,16 @@ extern "C" int delta_rule_pages(const int *cached, const int *fresh, const int *
     for (const void *p : ints)
         if ((uintptr_t)p & 3u) return DR_ERR_ALIGN;
     if ((uintptr_t)slots & 7u) return DR_ERR_ALIGN;
+    // every block reads the inputs (and the table) while others write: no output may share a byte with them
+    struct { const void *at; size_t bytes; } buf[] = {
+        {table, 4 * (size_t)R * width}, {lens, 4 * (size_t)R}, {cu_new, 4 * ((size_t)R + 1)},
+        {positions, 4 * (size_t)N}, {slots, 8 * (size_t)N}, {n_left, 4},
+        {cached, 4 * (size_t)R}, {fresh, 4 * (size_t)R}, {free_pages, 4 * (size_t)F}, {n_free, 4}};
+    for (int i = 0; i < 6; ++i)
+        for (int j = i + 1; j < 10; ++j) {
+            const uintptr_t a = (uintptr_t)buf[i].at, b = (uintptr_t)buf[j].at;
+            if (buf[i].bytes > 0 && buf[j].bytes > 0 && a < b + buf[j].bytes && b < a + buf[i].bytes) return DR_ERR_ARG;
+        }
     Pages p = {};
     p.cached = cached; p.fresh = fresh; p.free_pages = free_pages; p.n_free = n_free; p.table = table;
     p.lens = lens; p.cu_new = cu_new; p.positions = positions; p.n_left = n_left; p.slots = slots;

@@ -405,9 +405,10 @@ int delta_rule_clvr_bwd(const void *u, const void *W, const void *dh_out, void *
  *     n_left [1]     *n_free - the pages taken; negative: so many were missing
  * N is the batch's capacity; tokens behind it get no row.  Where the stack ran
  * short the table entry and the slots are -1; likewise the slots of tokens
- * behind the table's width (no page is taken for those).  N <= 2^30.  n_left
- * must not be n_free itself; the stack's entries are not changed, so the next
- * step passes n_left as its n_free.  A request that ends gives its pages back when
+ * behind the table's width (no page is taken for those).  N <= 2^30.  No output
+ * may overlap an input or another output (DR_ERR_ARG; lens is not cached itself,
+ * nor n_left n_free).  The stack's entries are not changed, so the next
+ * step passes lens as its cached and n_left as its n_free.  A request that ends gives its pages back when
  * the caller writes their numbers behind the top and raises the count.
  */
 int delta_rule_pages(const int *cached, const int *fresh, const int *free_pages, const int *n_free, int *table,

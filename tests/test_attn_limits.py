@@ -19,3 +19,35 @@ def test_reference_window_counts_back_from_a_length_behind_the_table():
     o, _ = oa.attn_decode(q, kc, vc, table, [12], window=5)
     assert np.allclose(o[0, 0], vc[0, 3, 0])
     assert np.array_equal(oa.attn_decode(q, kc, vc, table, [99])[0], oa.attn_decode(q, kc, vc, table, [8])[0])
+
+
+# ------------------------------------------------------------------------------------ refusals
+@pytest.fixture(scope="module")
+def binding():
+    from gated_delta_rule_107_b200 import binding, build
+    build.build()
+    binding.load()
+    return binding
+
+
+def test_pages_refuses_outputs_that_overlap(binding):
+    """Every block reads the lengths, the stack and its count while others write: an output that shares a
+    byte with an input or another output is refused.  No address here is ever read."""
+    R, F, width, page, N = 300, 500, 7, 16, 4000
+    sizes = dict(cached=4 * R, fresh=4 * R, free_pages=4 * F, n_free=4, table=4 * R * width, lens=4 * R, cu_new=4 * (R + 1),
+                 positions=4 * N, slots=8 * N, n_left=4)
+    names = list(sizes)
+    apart = {name: (i + 1) << 20 for i, name in enumerate(names)}
+
+    def call(**kw):
+        return binding.pages_raw(*{**apart, **kw}.values(), R, F, width, page, N, None)
+
+    for out in ("table", "lens", "cu_new", "positions", "slots", "n_left"):
+        for other in names:
+            if other == out:
+                continue
+            at = apart[other]
+            inside = at + (sizes[other] - 4) // 8 * 8          # the other's last whole word, or its only one
+            before = at - (sizes[out] - 4) // 8 * 8            # the output's last words on the other's first
+            for there in (at, inside, before):
+                assert call(**{out: there}) == binding.DR_ERR_ARG, (out, other, there - at)

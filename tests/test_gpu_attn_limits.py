@@ -289,3 +289,29 @@ def test_pages_small_outputs_do_not_hold_the_large_ones():
         assert t.untyped_storage().nbytes() <= 8 * R + 64
     few = binding.delta_rule_pages(cached, fresh, free, _i32([free.numel()]), table, 64, 100)  # all in one piece
     assert len({t.untyped_storage().data_ptr() for t in few}) == 1
+
+
+def test_pages_of_neighbouring_buffers():
+    """Buffers side by side in one allocation do not overlap; a table or a batch of no entries overlaps nothing."""
+    R, F, width, page, N = 3, 9, 8, 4, 40
+    mem = torch.zeros(4 * R + F + 3 + R * width + 4 + 3 * N + 8, dtype=torch.int32, device="cuda")
+    at, where = 0, {}
+    for name, n in (("slots", 2 * N), ("cached", R), ("fresh", R), ("free_pages", F), ("n_free", 1), ("table", R * width), ("lens", R),
+                    ("cu_new", R + 1), ("positions", N), ("n_left", 1)):
+        where[name] = mem[at:at + n]
+        at += n
+    cached, fresh = [7, 0, 30], [9, 12, 0]
+    for name, v in (("cached", cached), ("fresh", fresh), ("free_pages", list(range(20, 20 + F))), ("n_free", [F])):
+        where[name].copy_(_i32(v))
+    order = ("cached", "fresh", "free_pages", "n_free", "table", "lens", "cu_new", "positions", "slots", "n_left")
+    rc = binding.pages_raw(*(where[n].data_ptr() for n in order), R, F, width, page, N, torch.cuda.current_stream().cuda_stream)
+    torch.cuda.synchronize()
+    want = oa.pages(cached, fresh, list(range(20, 20 + F)), F, np.zeros((R, width)), page, N)
+    assert rc == binding.DR_OK
+    got = [where[n] for n in ("lens", "cu_new", "positions")] + [where["slots"].view(torch.int64), where["n_left"], where["table"].view(R, width)]
+    for a, b in zip(got, want):
+        assert (a.cpu().long() == torch.as_tensor(b).long()).all()
+    where["table"] = where["cached"]  # no columns
+    rc = binding.pages_raw(*(where[n].data_ptr() for n in order), R, F, 0, page, N, torch.cuda.current_stream().cuda_stream)
+    torch.cuda.synchronize()
+    assert rc == binding.DR_OK and (where["slots"].view(torch.int64) == -1).all()
