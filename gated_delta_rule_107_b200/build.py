@@ -46,24 +46,42 @@ KERNEL_FILES = {
 }
 
 
+def _key(cmd: list[str], torch) -> str:
+    """What the module of calls depends on: its sources (not where they lie), the command, torch and Python."""
+    import hashlib
+    import sysconfig
+    h = hashlib.sha256()
+    for part in (*(os.path.basename(c) if c in CALLS_SRC else c for c in cmd), torch.__version__, sysconfig.get_config_var("EXT_SUFFIX") or ""):
+        h.update(part.encode() + b"\0")
+    for p in CALLS_SRC:
+        with open(p, "rb") as f:
+            h.update(f.read())
+    return h.hexdigest()[:32]
+
+
 def build_calls(force: bool = False, verbose: bool = False) -> str:
-    """Compile csrc/torch_calls.cpp (host code against torch's and Python's headers) into _torch_calls.so."""
-    newest = max(os.path.getmtime(p) for p in CALLS_SRC)
-    if not force and os.path.exists(CALLS) and os.path.getmtime(CALLS) >= newest:
-        return CALLS
+    """Compile csrc/torch_calls.cpp (host code against torch's and Python's headers) into _torch_calls.so.
+
+    The module carries the key of what it was built from; one of another torch, Python or source is built again."""
     import sysconfig
 
     import torch
     t = os.path.join(os.path.dirname(torch.__file__))
     cuda = os.path.join(os.environ.get("CUDA_HOME", "/usr/local/cuda"), "include")
-    tmp = CALLS + f".tmp{os.getpid()}"
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-o", tmp, CALLS_SRC[0],
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", CALLS_SRC[0],
            "-isystem", os.path.join(t, "include"), "-isystem", os.path.join(t, "include", "torch", "csrc", "api", "include"),
            "-isystem", sysconfig.get_paths()["include"], "-isystem", cuda, "-L" + os.path.join(t, "lib"),
            "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch", "-ltorch_python",
            # torch's own C++ runtime: a second, static one would not know torch's exceptions
-           "-nostdlib++", "-l:libstdc++.so.6"]
+           "-nodefaultlibs", "-l:libstdc++.so.6", "-lm", "-lgcc_s", "-lgcc", "-lc"]
+    key = _key(cmd, torch)
+    if not force and os.path.exists(CALLS):
+        with open(CALLS, "rb") as f:
+            if key.encode() in f.read():
+                return CALLS
+    tmp = CALLS + f".tmp{os.getpid()}"
+    cmd += [f'-DCALLS_KEY="{key}"', "-o", tmp]
     if verbose:
         print(" ".join(cmd))
     subprocess.check_call(cmd)
@@ -71,9 +89,8 @@ def build_calls(force: bool = False, verbose: bool = False) -> str:
     return CALLS
 
 
-def build(force: bool = False, verbose: bool = False, extra: list[str] | None = None) -> str:
-    """Compile csrc/delta_rule_lib.cu (the unity translation unit) into libdeltarule.so, and csrc/torch_calls.cpp."""
-    build_calls(force, verbose)
+def build_library(force: bool = False, verbose: bool = False, extra: list[str] | None = None) -> str:
+    """Compile csrc/delta_rule_lib.cu (the unity translation unit) into libdeltarule.so; needs nvcc and nothing else."""
     newest = max(os.path.getmtime(p) for p in sources())
     if not force and os.path.exists(LIB) and os.path.getmtime(LIB) >= newest:
         return LIB
@@ -85,6 +102,18 @@ def build(force: bool = False, verbose: bool = False, extra: list[str] | None = 
     subprocess.check_call(cmd)
     os.replace(tmp, LIB)
     return LIB
+
+
+def build(force: bool = False, verbose: bool = False, extra: list[str] | None = None) -> str:
+    """The library, and then the module of calls on torch tensors, where there is a torch."""
+    lib = build_library(force, verbose, extra)
+    try:
+        import torch  # noqa: F401
+    except ImportError:
+        print("no torch: _torch_calls.so, the calls of the softmax-attention layers on its tensors, is not built")
+        return lib
+    build_calls(force, verbose)
+    return lib
 
 
 if __name__ == "__main__":

@@ -423,4 +423,12 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_torch_calls", nullptr, -1, method
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__torch_calls(void) { return PyModule_Create(&module); }
+#ifndef CALLS_KEY
+#define CALLS_KEY ""
+#endif
+// `built_from`: the key of the sources, the command, torch and Python that the module was built from
+PyMODINIT_FUNC PyInit__torch_calls(void) {
+    PyObject *m = PyModule_Create(&module);
+    if (m && PyModule_AddStringConstant(m, "built_from", CALLS_KEY) != 0) Py_CLEAR(m);
+    return m;
+}

@@ -51,3 +51,51 @@ def test_pages_refuses_outputs_that_overlap(binding):
             before = at - (sizes[out] - 4) // 8 * 8            # the output's last words on the other's first
             for there in (at, inside, before):
                 assert call(**{out: there}) == binding.DR_ERR_ARG, (out, other, there - at)
+
+
+# ------------------------------------------------------------------------------------ the build
+@pytest.fixture
+def build(tmp_path, monkeypatch):
+    """The build with compilers that only write what they were asked for, into a folder of its own."""
+    from gated_delta_rule_107_b200 import build as b
+    fake = tmp_path / "compiler"
+    fake.write_text('#!/bin/sh\nall="$*"\necho "$all" >> ' + str(tmp_path / "calls") + '\nwhile [ "$1" != -o ]; do shift; done\n'
+                    'echo "$all" > "$2"\n')
+    fake.chmod(0o755)
+    monkeypatch.setenv("NVCC", str(fake))
+    monkeypatch.setenv("CXX", str(fake))
+    monkeypatch.setattr(b, "LIB", str(tmp_path / "libdeltarule.so"))
+    monkeypatch.setattr(b, "CALLS", str(tmp_path / "_torch_calls.so"))
+    b.calls = lambda: (tmp_path / "calls").read_text().count("torch_calls.cpp") if (tmp_path / "calls").exists() else 0
+    yield b
+    del b.calls
+
+
+def test_the_library_is_built_where_the_torch_module_cannot_be(build, monkeypatch, tmp_path):
+    """libdeltarule.so needs nvcc and nothing else."""
+    import os
+    import subprocess
+    import sys
+    no = tmp_path / "no"
+    no.write_text("#!/bin/sh\nexit 1\n")
+    no.chmod(0o755)
+    monkeypatch.setenv("CXX", str(no))
+    with pytest.raises(subprocess.CalledProcessError):
+        build.build(force=True)
+    assert os.path.exists(build.LIB) and not os.path.exists(build.CALLS)
+    os.remove(build.LIB)
+    monkeypatch.setitem(sys.modules, "torch", None)  # importing it raises ImportError
+    assert build.build(force=True) == build.LIB
+    assert os.path.exists(build.LIB) and not os.path.exists(build.CALLS)
+
+
+def test_the_torch_module_is_built_again_for_another_torch(build, monkeypatch):
+    """File times do not show that torch, Python or the flags changed."""
+    import torch
+    build.build_calls()
+    build.build_calls()
+    assert build.calls() == 1
+    monkeypatch.setattr(torch, "__version__", "9.9.9")
+    build.build_calls()
+    build.build_calls()
+    assert build.calls() == 2
