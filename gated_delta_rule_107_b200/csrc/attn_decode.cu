@@ -302,7 +302,8 @@ template <typename E, int D, int TILE_, int STAGES> struct Pipe {
 // Each keeps, for the heads of a block, m (base 2), l and o, and offers
 //   fetch(q row of the block's first head, heads): reads the queries; begin(): they are the ones from now
 //   tile(stage, live)
-//   finish(m, l, o): l summed over lanes, all three to shared memory, o as [head][slot_of(head, channel)]
+//   finish(m, l, o): l summed over lanes, all three to shared memory, o as [head][slot_of(head, channel)];
+//     l = 0 and o = 0 where no score was above -inf, whatever the values hold
 
 // where a head's channel lies in a row of o in shared memory: blocks of 8 channels exchanged so that
 // the matrix fragments (8 channels of four pairs of heads at once) fall into different banks
@@ -472,9 +473,10 @@ template <int D, int NT> struct Mma {  // bf16: blocks of 8 NT heads
 #pragma unroll
                 for (int d = 4; d < 32; d <<= 1) l[j][i] += __shfl_xor_sync(0xffffffffu, l[j][i], d);
                 const int head = j * 8 + 2 * t + i;
+                const float sum = sum_of(m[j][i], l[j][i]);
                 if (g == 0) {
                     sm[head] = m[j][i];
-                    sl[head] = sum_of(m[j][i], l[j][i]);
+                    sl[head] = sum;
                 }
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k)
@@ -482,7 +484,7 @@ template <int D, int NT> struct Mma {  // bf16: blocks of 8 NT heads
                     for (int c = 0; c < 2; ++c) {
                         float x[2];
                         un(o[k][j][c], x[0], x[1]);
-                        so[head * D + slot_of(head, k * 16 + 8 * c + g)] = x[i];
+                        so[head * D + slot_of(head, k * 16 + 8 * c + g)] = sum == 0.f ? 0.f : x[i];
                     }
             }
     }
@@ -625,11 +627,13 @@ template <int D, int H> struct Simt {
         for (int c = 0; c < C; ++c) {
 #pragma unroll
             for (int d = LT; d < 32; d <<= 1) l[c] += __shfl_xor_sync(0xffffffffu, l[c], d);
+            l[c] = sum_of(m[c], l[c]);
             if (first() && token() == 0) {
                 sm[head() + c] = m[c];
-                sl[head() + c] = sum_of(m[c], l[c]);
+                sl[head() + c] = l[c];
             }
         }
+        __syncwarp();
 #pragma unroll
         for (int h = 0; h < GB; ++h) {
             float x[4];
@@ -639,7 +643,9 @@ template <int D, int H> struct Simt {
             for (int d = LR; d < 32; d <<= 1)  // the rows side by side
 #pragma unroll
                 for (int c = 0; c < 4; ++c) x[c] += __shfl_xor_sync(0xffffffffu, x[c], d);
-            if (lane < LR) *reinterpret_cast<float4 *>(so + h * D + slot_of(h, 4 * lane)) = make_float4(x[0], x[1], x[2], x[3]);
+            if (lane < LR)
+                *reinterpret_cast<float4 *>(so + h * D + slot_of(h, 4 * lane)) =
+                    sl[h] == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(x[0], x[1], x[2], x[3]);
         }
     }
 };

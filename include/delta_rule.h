@@ -469,9 +469,9 @@ int delta_rule_qkrope_cache(const void *q, const void *k, const void *v, const f
  * (lse fp32, NULL = not written; window = 0: all tokens).  A request that sees no
  * token, or only scores of -inf, gets out = 0, lse = -inf.  Tokens behind the table's width, and tokens
  * whose table entry is no page (outside [0, n_pages)), are not seen; what their
- * rows hold is not read.  An infinite value that is seen makes its channel of out
- * infinite whatever its weight (NaN with one of the other sign, or where all
- * scores are -inf).  Sums and softmax statistics are fp32.  Results do not
+ * rows hold is not read.  An infinite value whose score is above -inf makes its
+ * channel of out infinite, however small its weight (NaN with one of the other
+ * sign).  Sums and softmax statistics are fp32.  Results do not
  * change from run to run.  R * Hq * (width * page + 64) must stay below 2^41
  * (DR_ERR_UNSUPPORTED).  The workspace is
  * delta_rule_attn_decode_workspace_size(Hq, Hk, d, dtype) bytes (whatever the

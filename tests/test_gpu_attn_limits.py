@@ -7,7 +7,7 @@ import torch
 from gated_delta_rule_107_b200 import binding
 from oracle import attn as oa
 from parity_util import np64
-from test_gpu_attn import DT, HALF, _i32
+from test_gpu_attn import DT, HALF, _check_attn, _i32
 
 pytestmark = pytest.mark.gpu
 
@@ -315,3 +315,29 @@ def test_pages_of_neighbouring_buffers():
     rc = binding.pages_raw(*(where[n].data_ptr() for n in order), R, F, 0, page, N, torch.cuda.current_stream().cuda_stream)
     torch.cuda.synchronize()
     assert rc == binding.DR_OK and (where["slots"].view(torch.int64) == -1).all()
+
+
+@pytest.mark.parametrize("dtype", ("f32", "bf16"))
+@pytest.mark.parametrize("d,Hq,Hk", ((64, 2, 1), (128, 12, 1), (64, 32, 2), (128, 8, 8)))
+def test_attn_decode_values_without_weight(dtype, d, Hq, Hk):
+    """Only scores of -inf: out = 0 and lse = -inf whatever the values hold, and such a part of a request
+    adds nothing to the others."""
+    lens = [40, 3000, 1]
+    page, width = 16, 188
+    g = torch.Generator().manual_seed(d)
+    kc, vc = (torch.randn(3 * width, page, Hk, d, generator=g).to(DT[dtype]).cuda() for _ in range(2))
+    q = torch.ones(3, Hq, d, dtype=DT[dtype], device="cuda")
+    table = torch.arange(3 * width, dtype=torch.int32, device="cuda").view(3, width)
+    for r in (0, 2):
+        kc[table[r].long()] = float("-inf")
+        vc[table[r].long()] = float("inf")
+        vc[table[r].long(), 3, :, 5] = float("nan")
+    k1, v1 = kc[table[1].long()].clone(), vc[table[1].long()].clone()
+    kc[table[1, 10:120].long()] = float("-inf")  # finite values: nothing of them is seen
+    o, lse = binding.delta_rule_attn_decode(q, kc, vc, table, _i32(lens), want_lse=True)
+    short = torch.cat([table[1:2, :10], table[1:2, 120:]], 1).contiguous()
+    kc[table[1].long()], vc[table[1].long()] = k1, v1
+    torch.cuda.synchronize()
+    for r in (0, 2):
+        assert (o[r] == 0).all() and torch.isneginf(lse[r]).all(), r
+    _check_attn(o[1:2], lse[1:2], q[1:2], kc, vc, short, [3000 - 110 * 16], dtype)
