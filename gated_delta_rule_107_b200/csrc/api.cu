@@ -935,7 +935,7 @@ extern "C" int delta_rule_qkrope_cache(const void *q, const void *k, const void 
     if (rc != DR_OK) return rc;
     if (Hk < 1 || n_pages < 0 || page <= 0) return DR_ERR_ARG;
     if (N == 0) return DR_OK;
-    if (!positions || !slots || !v || !k_cache || !v_cache || (Hq > 0 && !q_out)) return DR_ERR_ARG;
+    if (!positions || !slots || !v || (n_pages > 0 && (!k_cache || !v_cache)) || (Hq > 0 && !q_out)) return DR_ERR_ARG;
     rc = check_stride(v_stride, (long long)Hk * d, dtype);
     if (rc == DR_OK) rc = check_cache(k_page_stride, k_token_stride, k_head_stride, d, dtype, &p.kcs);
     if (rc == DR_OK) rc = check_cache(v_page_stride, v_token_stride, v_head_stride, d, dtype, &p.vcs);

@@ -341,3 +341,17 @@ def test_attn_decode_values_without_weight(dtype, d, Hq, Hk):
     for r in (0, 2):
         assert (o[r] == 0).all() and torch.isneginf(lse[r]).all(), r
     _check_attn(o[1:2], lse[1:2], q[1:2], kc, vc, short, [3000 - 110 * 16], dtype)
+
+
+@pytest.mark.parametrize("dtype", ("f32", "bf16"))
+def test_qkrope_cache_without_pages(dtype):
+    """A cache of no pages, as the attention over it takes it: the queries come out, nothing is written."""
+    g = torch.Generator().manual_seed(3)
+    x = torch.randn(5, 6, 64, generator=g).to(DT[dtype]).cuda()
+    none = torch.empty(0, 16, 2, 64, dtype=DT[dtype], device="cuda")
+    pos, slots = _i32([0, 1, 2, 3, 4]), torch.tensor([-1, 0, 5, -1, 2 ** 40], device="cuda")
+    f = 100.0 ** (-torch.arange(0, 64, 2, dtype=torch.float64) / 64).cuda()
+    q = binding.delta_rule_qkrope_cache(x[:, :2], x[:, 2:4], x[:, 4:], None, None, f, pos, slots, none, none.clone())
+    want, _ = binding.delta_rule_qkrope(x[:, :2], x[:, 2:4], None, None, f, pos)
+    torch.cuda.synchronize()
+    assert torch.equal(q, want)
