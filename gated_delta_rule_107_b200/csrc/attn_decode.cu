@@ -8,9 +8,10 @@
 //
 // What bounds it is reading the cache once: a key head's rows serve the G = Hq / Hk heads of its
 // group, 2 G flops a byte in bf16, far below what the tensor cores need to be busy; so the design
-// is about bytes in flight (128 KB an SM) and an even split.  Three requests of 200001 tokens (1.23 GB)
-// are read at 6.5 TB/s, the rate of a plain copy, 64 ragged ones of up to 16384 (540 MB) at 6.0; small
-// calls are the chain of launch, lengths, table, rows, join: 7.5 us for one request of 2000 tokens.
+// is about bytes in flight (128 KB an SM) and an even split.  In calls replayed in a graph three requests
+// of 200001 tokens (1.23 GB) are read at 6.6 TB/s, the rate of a plain copy, 64 ragged ones of up to 16384
+// (540 MB) at 5.9; behind other kernels on a stream at 6.4 and 5.7.  Small calls are the chain of launch,
+// lengths, table, rows, join: 7.8 us for one request of 2000 tokens.
 //   Work.  The piece is a tile of tokens of one (request, key head[, block of its query heads]): as
 //     many as make 4 KB of keys and 4 KB of values (8, 16 or 32).  The tiles of all requests form one
 //     list, cut into equal contiguous runs, one per CTA, however ragged the lengths: a run may hold
@@ -34,13 +35,14 @@
 //     (with two, 2^-17 of p, outputs that are small against the values were off by more than fp32 sums
 //     are), and a tile's products are summed from zero and then added to o in fp32: the tensor cores
 //     cut what they add to a sum, and cutting the running sum a thousand times lost 2^-16 of it.  The
-//     additional products hide behind the loads as long as several are in flight (three requests
-//     of 200001 tokens 183.3 us, as with two products into the running sum; with a kernel of 168
-//     registers and so fewer in flight 194), less so in wide groups (32 of 6103, groups of 16, 29.7 ->
-//     31.3).  Groups of 16 reach 79 to 83 % of the copy's rate, of 32 43 %.
+//     additional products hide behind the loads as long as several are in flight (three requests of
+//     200001 tokens: 187.3 us in a graph, 192 on a stream; with two products into the running sum 186.5
+//     and 188; with a kernel of 168 registers, and so fewer in flight, 194 and 201), less so in wide
+//     groups.  For 400 MB groups of up to 8 heads reach 87 % of the copy's rate (64 channels 77 %), of 16
+//     73 % (65 %; with two products 78 and 69 %), of 32 38 % (34 %).
 //   fp32.  CUDA cores, 1, 2, 4 or up to 8 heads at a time, packed arithmetic: a lane holds 4 channels
-//     of the heads' queries and outputs.  Groups of up to 4 are bound by the loads (87 to 94 % of the
-//     copy's rate), of 8 by two warps a scheduler working through their tiles (68 to 70 %).
+//     of the heads' queries and outputs.  For 400 MB groups of up to 4 are bound by the loads (86 to 92 %
+//     of the copy's rate), of 8 by two warps a scheduler working through their tiles (61 to 69 %).
 // Tokens that are masked (or whose table entry is no page) are neither read nor seen: their rows
 // in shared memory are zero-filled, their scores -inf.  A request with none gives o = 0, lse = -inf.
 #include <math_constants.h>

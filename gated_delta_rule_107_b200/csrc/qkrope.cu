@@ -16,9 +16,11 @@
 // fraction is then exact enough in 32 bits.
 //
 // What bounds it is moving each element twice (forward) or three times (backward).  At 8 x 4096
-// tokens of 10 heads of 128 channels in bf16: forward 30.3 us for 168 MB (5.5 TB/s, 86 % of a plain
-// copy's rate), backward 45.5 us for 252 MB (86 %); 8192 tokens of 16 + 2 + 2 heads into the cache
-// 14.2 us for 84 MB (91 %).  To get there the loads run ahead through shared memory (with loads into
+// tokens of 10 heads of 128 channels in bf16: forward 30.6 us for 168 MB (5.5 TB/s, 85 % of a plain
+// copy's rate), backward 46.0 us for 252 MB (85 %), in calls replayed in a graph; 31.6 and 47.8 (82 %)
+// behind other kernels on a stream.  8192 tokens of 16 + 2 + 2 heads into the cache, 84 MB: 14.5 us (89 %)
+// in a graph, 18.2 (71 %) on a stream, most likely because its 256 blocks, a wave that is not full, fall
+// unevenly on the SMs there.  To get there the loads run ahead through shared memory (with loads into
 // registers the forward took 50.8 us, its warps waiting), the arithmetic is packed (without, 70 % of
 // all issue slots were taken), and neighbouring lanes always hold neighbouring vectors (with the
 // channels behind rot two vectors a lane side by side, 32768 tokens with half of the channels

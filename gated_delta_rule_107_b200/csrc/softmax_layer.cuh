@@ -78,8 +78,9 @@ inline cudaError_t launch_after(void (*kern)(P...), dim3 grid, dim3 block, size_
 }
 // Nothing of global memory is touched before after_previous().  let_next() stands where a block's
 // work ends, unless the next kernel is known to be small: blocks that are placed while others of
-// this kernel still hold their SMs fall unevenly (a call whose 256 blocks began so took 18.0 us
-// instead of 14.5).
+// this kernel still hold their SMs fall unevenly (a call of 256 blocks, replayed in a graph: 18.0 us
+// with the trigger at its start, 14.5 with it at the end; behind another library's kernel on a stream such a
+// call takes 18 us wherever the trigger stands).
 __device__ __forceinline__ void after_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void let_next() { asm volatile("griddepcontrol.launch_dependents;"); }
 
